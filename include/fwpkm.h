@@ -392,6 +392,164 @@ fwpkm_status fwpkm_addressing_metrics(const int32_t* idx, int num_mem, int T, in
                                       void* workspace, size_t ws_bytes, double* metrics, int64_t* counts,
                                       void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Lookups of a learned table (a token embedding; a product-key value table trained as
+ * slow weights, "Fast-weight Product Key Memory" (paperlayer summary) §2.2, whose slots
+ * and weights are fwpkm_forward_chunk's idx_out and w_out), and their gradients:
+ *   out_t     = scale * sum_{r < R} w[t][r] table[idx[t][r]]        (w NULL: ones)
+ *   dtable_i  = scale * sum_{(t,r): idx[t][r] = i} w[t][r] dout_t
+ *   dw[t][r]  = scale * <dout_t, table[idx[t][r]]>
+ * Entries of idx outside [0, rows) contribute nothing (padding: any negative index).
+ * Sums are fp32, each result rounded once to its type.  Rows are read 16 bytes at a time
+ * when width, strides and pointers allow it; any element alignment works.
+ * ------------------------------------------------------------------------- */
+typedef enum { FWPKM_I32 = 0, FWPKM_I64 = 1 } fwpkm_index_dtype;
+
+/* Supported limits (else FWPKM_ERR_UNSUPPORTED): rows < 2^31 - 1, width <= 2^20,
+ * R <= 1024, n * R < 2^31. */
+typedef struct {
+  long long rows;     /* rows of the table                                        */
+  long long table_ld; /* elements between rows of the table (>= width)            */
+  long long out_ld;   /* elements between rows of out and d_out (>= width)        */
+  int width;
+  int R;              /* rows per token; w and idx are [n][R]                     */
+  int dtype;          /* fwpkm_dtype of table, out and d_out                      */
+  int idx_dtype;      /* fwpkm_index_dtype of idx                                 */
+  float scale;
+} fwpkm_lookup_config;
+
+/* out [n][width] of n tokens.  w is fp32 or NULL.  n = 0 is a no-op. */
+fwpkm_status fwpkm_lookup(const fwpkm_lookup_config* cfg, const void* table, const void* idx, const float* w,
+                          long long n, void* out, void* stream);
+
+/* Bytes of device workspace (256-byte aligned, contents need not be initialised) of a
+ * backward call for n tokens that forms d_table. */
+fwpkm_status fwpkm_lookup_backward_workspace_size(const fwpkm_lookup_config* cfg, long long n, size_t* bytes);
+
+/* Gradients of fwpkm_lookup from d_out [n][width].
+ *   d_table  [rows] rows of `width`, grad_ld elements apart, of type grad_dtype; NULL: not
+ *            formed (then the workspace may be NULL).  accumulate = 0: every row is written
+ *            (zero where nothing was read; also for n = 0); else the gradient is added to
+ *            the rows that were read and the others are left as they were.
+ *   dw       fp32 [n][R] or NULL; needs the table.
+ *   table    read for dw only (else may be NULL).
+ * The pairs are sorted by row, so each row's terms are summed in a fixed order.  The
+ * workspace must not be shared with a call that may run at the same time. */
+fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* table, const void* idx, const float* w,
+                                   const void* d_out, long long n, void* d_table, long long grad_ld, int grad_dtype,
+                                   int accumulate, float* dw, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Balance of a router over its experts (experts of a layer, sub-keys of a codebook): the
+ * loss on the logits, the experts' counts, and the gradient.  Per group, over the tokens
+ * that the mask leaves (P_t = softmax(x_t), T of them):
+ *   usage u = (1/T) sum_t P_t,  counts c_e = selections of expert e,  f = c / sum c
+ *   FWPKM_BALANCE_LOAD     loss = coef E sum_e f_e u_e         (a_e = E f_e)
+ *   FWPKM_BALANCE_ENTROPY  loss = coef sum_e u_e log u_e       (a_e = log u_e + 1; with
+ *       coef 1 the -H of the memory's addressing loss, "Fast-weight Product Key Memory"
+ *       (paperlayer summary) §3.4)
+ *   dx_t[e] = d_loss (coef / T) P_t[e] (a_e - sum_e' a_e' P_t[e'])   (counts: constants)
+ * A group without a token has loss, usage and gradient 0.  Logits of -inf have P = 0; a row
+ * of nothing else is left out like a masked one (its selections still count).  What a
+ * masked row holds, NaN included, is not read; its dx is 0.
+ * ------------------------------------------------------------------------- */
+typedef enum { FWPKM_BALANCE_LOAD = 0, FWPKM_BALANCE_ENTROPY = 1 } fwpkm_balance_kind;
+
+/* Supported limits (else FWPKM_ERR_UNSUPPORTED): experts <= 4096, k <= 4096,
+ * groups <= 65535, tokens * k < 2^31. */
+typedef struct {
+  long long tokens;       /* T, tokens per group                                    */
+  long long ld;           /* elements between a group's rows of x (>= experts)      */
+  long long group_stride; /* elements between the groups of x                       */
+  int groups;
+  int experts;            /* E                                                      */
+  int k;                  /* selections per token in idx (0 without idx)            */
+  int dtype;              /* fwpkm_dtype of x and dx                                */
+  int kind;               /* fwpkm_balance_kind                                     */
+  float coef;
+} fwpkm_balance_config;
+
+/* Bytes of device workspace (256-byte aligned, contents need not be initialised). */
+fwpkm_status fwpkm_balance_workspace_size(const fwpkm_balance_config* cfg, size_t* bytes);
+
+/*   x       [groups][tokens][experts] logits (ld, group_stride)
+ *   idx     int32 [groups][tokens][k] selected experts, or NULL (entropy only: then counts
+ *           are 0); entries outside [0, experts) are not counted
+ *   mask    one byte per token [groups][tokens], 0 = left out; NULL: every token counts
+ *   loss fp32 [groups], counts int32 [groups][experts] (NULL: not wanted),
+ *   usage fp32 [groups][experts], slope fp32 [groups][experts] (what the backward needs of
+ *   the forward: (coef / T)(a_e less a constant, which the gradient does not see)). */
+fwpkm_status fwpkm_balance_loss(const fwpkm_balance_config* cfg, const void* x, const int32_t* idx,
+                                const uint8_t* mask, void* workspace, size_t ws_bytes, float* loss, int32_t* counts,
+                                float* usage, float* slope, void* stream);
+
+/* dx [groups][tokens][experts] (contiguous, the type of x) from the same x and mask, the
+ * forward's slope and d_loss fp32 [groups] (NULL: ones). */
+fwpkm_status fwpkm_balance_loss_backward(const fwpkm_balance_config* cfg, const void* x, const uint8_t* mask,
+                                         const float* slope, const float* d_loss, void* dx, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the dense fast-weight memory (one d x d_v
+ * matrix per sequence and head, written by every token) next to which the sparse memory is
+ * used.  With a = exp(log_decay[h]):
+ *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   S before the first token = s0.
+ * log_decay is a constant of the heads (fp32 [H], normally <= 0; -inf: S_t = k_t v_t^T); it
+ * gets no gradient.  States are fp32 [B][H][d][d_v], contiguous; q, k, v, o and their
+ * gradients fp32 or bf16 (cfg.dtype).  Sums and states are held in fp32; bf16 prompts run
+ * on the tensor cores, where fp32 operands enter as enough bf16 pieces that results agree
+ * with fp32 arithmetic.
+ * ------------------------------------------------------------------------- */
+
+/* One tensor of all heads: element (b, h, t, e) at p[b*sb + h*sh + t*st + e], any strides of
+ * at least 0 (0 broadcasts an input; the rows of an output must not share memory). */
+typedef struct {
+  void* p;
+  long long sb, sh, st;
+} fwpkm_heads;
+
+/* Supported limits (else FWPKM_ERR_UNSUPPORTED): d, d_v <= 256, B * H <= 2^24, T <= 2^28. */
+typedef struct {
+  int B, H;    /* sequences, heads per sequence                                    */
+  int d, d_v;  /* widths of q, k and of v, o                                       */
+  int dtype;   /* fwpkm_dtype of q, k, v, o and their gradients                    */
+  float scale; /* not 0                                                            */
+} fwpkm_linattn_config;
+
+/* Bytes of device workspace (256-byte aligned, contents need not be initialised) of a call
+ * over T tokens; may be 0 (then the workspace may be NULL). */
+fwpkm_status fwpkm_linear_attention_workspace_size(const fwpkm_linattn_config* cfg, int T, int backward,
+                                                   size_t* bytes);
+
+/* A prompt (or training batch) of T tokens.
+ *   lens   int32 [B] or NULL: sequence b has lens[b] tokens (clamped to [0, T]); tokens
+ *          behind them are not read and their rows of o left as they were.
+ *   s0     start states or NULL (zeros);  sT  states after each sequence's last token, or
+ *          NULL; sT may be s0's memory.
+ * T = 0: o is not touched, sT = s0.  The workspace must not be shared with a call that may
+ * run at the same time. */
+fwpkm_status fwpkm_linear_attention(const fwpkm_linattn_config* cfg, const fwpkm_heads* q, const fwpkm_heads* k,
+                                    const fwpkm_heads* v, int T, const float* log_decay, const int32_t* lens,
+                                    const float* s0, const fwpkm_heads* o, float* sT, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
+/* Its gradients from d_o (the layout of o) and d_sT (NULL: zero): dq, dk, dv, and ds0 (NULL:
+ * not wanted; may be d_sT's memory).  Rows behind a sequence's end are left as they were.
+ * dq, dk, dv must not be the memory of q, k, v, d_o. */
+fwpkm_status fwpkm_linear_attention_backward(const fwpkm_linattn_config* cfg, const fwpkm_heads* q,
+                                             const fwpkm_heads* k, const fwpkm_heads* v, int T,
+                                             const float* log_decay, const int32_t* lens, const float* s0,
+                                             const fwpkm_heads* d_o, const float* d_sT, const fwpkm_heads* dq,
+                                             const fwpkm_heads* dk, const fwpkm_heads* dv, float* ds0,
+                                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Token-at-a-time form: n_tok tokens of every sequence in one launch without a workspace.
+ * `state` is read and `state_out` written (the same memory: in place).  lens as above: a
+ * sequence with no token keeps its state and its rows of o. */
+fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const fwpkm_heads* q, const fwpkm_heads* k,
+                                         const fwpkm_heads* v, int n_tok, const float* log_decay,
+                                         const int32_t* lens, const float* state, const fwpkm_heads* o,
+                                         float* state_out, void* stream);
+
 /* Wait for `stream` and return the latched device status (FWPKM_OK,
  * FWPKM_ERR_TIMEOUT, FWPKM_ERR_BAD_SLOT), clearing it (device word and host copy). */
 fwpkm_status fwpkm_sync(fwpkm_state* st, void* stream);

@@ -1,0 +1,514 @@
+// balance.cu -- how evenly a router uses its experts (sub-keys, slots): a balance loss on its
+// logits, the experts' counts, and the loss's gradient.
+//
+// Per group (a layer, a sequence, one half of a memory's codebook) with logits x [T][E]:
+//   P_t = softmax(x_t),  u = mean_t P_t (usage),  c_e = selections of expert e (counts)
+//   load:     L = coef E sum_e f_e u_e,   f = c / sum c       (a_e = E f_e)
+//   entropy:  L = coef sum_e u_e log u_e  (= -coef H(u), the memory's own anti-collapse loss,
+//             Fast-weight Product Key Memory (paperlayer summary) §3.4; a_e = log u_e + 1)
+//   dx_t[e] = dL coef / T P_t[e] (a_e - sum_e' a_e' P_t[e'])
+// over the T tokens that the mask leaves (counts are constants of the gradient).  A row whose
+// logits are all -inf has no softmax: it is left out like a masked one, but its selections
+// count.  The gradient does not see a constant added to a, so the forward stores the slope
+// coef (a - const) / T with the constant that a balanced router has (E f - 1, log(E u)):
+// what is left in the bracket then does not cancel in fp32.
+//
+// Bytes: x read once per direction, dx written once; ~8 operations per logit: bound by HBM.
+// Forward: CTAs over blocks of a group's rows, a team of lanes per row with the row in
+// registers (one read), column sums in registers over the team's rows, joined over the
+// CTA's teams in team order; a second launch joins the CTAs' partial sums in order, in fp64.
+// No float atomics, so the results are deterministic; the counts are integer sums.
+#include <cstdio>
+
+#include "fwpkm_internal.cuh"
+
+namespace fwpkm {
+namespace {
+
+constexpr int BL_THREADS = 512;
+constexpr int BL_MAX_E = 4096;
+constexpr int BL_JOIN = 1024;
+
+struct BalArgs {
+  const void* x;
+  long long ld, gs;        // elements between a group's rows, and between groups
+  const int32_t* idx;      // [G][T][k] or null
+  const uint8_t* mask;     // [G][T] or null
+  int G, E, k, ctas;       // ctas: per group
+  long long T, rows_cta;   // rows per CTA
+  float* part;             // [G][ctas][E] partial usage sums
+  int32_t* cpart;          // [G][ctas][E] partial counts
+  int32_t* npart;          // [G][ctas] rows with a softmax
+};
+
+template <typename T, int VEC>
+struct __align__(sizeof(T) * VEC) BPack {
+  T v[VEC];
+};
+__device__ __forceinline__ float bal_f(float x) { return x; }
+__device__ __forceinline__ float bal_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void bal_put(float& d, float x) { d = x; }
+__device__ __forceinline__ void bal_put(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+
+// A row of E logits over a team of L lanes (L <= 32: lanes of a warp; L = BL_THREADS: the
+// CTA): thread `l` holds elements (j L + l) VEC .. +VEC-1, j < NCH; -inf past E.
+template <typename T, int VEC, int NCH, int L>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l, float (&v)[VEC * NCH]) {
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    const int e = (j * L + l) * VEC;
+    if (e < E) {
+      const BPack<T, VEC> p = *reinterpret_cast<const BPack<T, VEC>*>(row + e);
+#pragma unroll
+      for (int u = 0; u < VEC; ++u) v[j * VEC + u] = bal_f(p.v[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < VEC; ++u) v[j * VEC + u] = -INFINITY;
+    }
+  }
+}
+
+template <int L, bool MAX>
+__device__ __forceinline__ float team_reduce(float x, float* red) {
+  constexpr int W = L < 32 ? L : 32;
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
+  if (L > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = red[0];
+#pragma unroll
+    for (int w = 1; w < L / 32; ++w) x = MAX ? fmaxf(x, red[w]) : x + red[w];
+  }
+  return x;
+}
+
+// v -> softmax(v) over the team; false (v = 0) for a row without a finite logit.  The maximum
+// passes NaN by, but the sum keeps it.
+template <int NV, int L>
+__device__ __forceinline__ bool team_softmax(float (&v)[NV], float* red) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
+  m = team_reduce<L, true>(m, red);
+  float s = 0.f;
+  const bool none = m == -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = none && !isnan(v[i]) ? 0.f : expf(v[i] - m);
+    s += v[i];
+  }
+  s = team_reduce<L, false>(s, red);
+  if (s == 0.f) return false;
+  const float inv = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] *= inv;
+  return true;
+}
+
+template <typename T, int VEC, int NCH, int L>
+__global__ void __launch_bounds__(BL_THREADS)
+balance_sum_kernel(BalArgs a) {
+  constexpr int NV = VEC * NCH;
+  constexpr int TEAMS = BL_THREADS / L;
+  extern __shared__ float sm[];               // [TEAMS][L * NV] usage sums, then counts [E]
+  __shared__ float red[BL_THREADS / 32];
+  __shared__ int s_n;
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.y, cta = blockIdx.x;
+  const int team = threadIdx.x / L, l = threadIdx.x % L;
+  const long long t0 = (long long)cta * a.rows_cta;
+  const long long t1 = t0 + a.rows_cta < a.T ? t0 + a.rows_cta : a.T;
+  const T* x = (const T*)a.x + (long long)g * a.gs;
+  const uint8_t* mask = a.mask ? a.mask + (long long)g * a.T : nullptr;
+  int* cnt = (int*)(sm + TEAMS * L * NV);
+  if (threadIdx.x == 0) s_n = 0;
+  if (a.idx)
+    for (int e = threadIdx.x; e < a.E; e += BL_THREADS) cnt[e] = 0;
+  float acc[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+  int n = 0;
+  __syncthreads();
+  // every team of a warp takes part in the warp's shuffles, so the loop's trip count is the CTA's
+  for (long long tb = t0; tb < t1; tb += TEAMS) {
+    const long long t = tb + team;
+    const bool on = t < t1 && (!mask || mask[t]);
+    float v[NV];
+    if (on) {
+      load_row<T, VEC, NCH, L>(x + t * a.ld, a.E, l, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = -INFINITY;
+    }
+    if (team_softmax<NV, L>(v, red)) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) acc[i] += v[i];
+      n += l == 0;
+    }
+  }
+  if (n) atomicAdd(&s_n, n);
+  if (a.idx) {
+    const int32_t* ix = a.idx + (long long)g * a.T * a.k;
+    for (long long p = t0 * a.k + threadIdx.x; p < t1 * a.k; p += BL_THREADS) {
+      const int e = ix[p];
+      if (e >= 0 && e < a.E && (!mask || mask[p / a.k])) atomicAdd(&cnt[e], 1);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int u = 0; u < VEC; ++u) sm[team * (L * NV) + (j * L + l) * VEC + u] = acc[j * VEC + u];
+  __syncthreads();
+  float* part = a.part + ((long long)g * a.ctas + cta) * a.E;
+  for (int e = threadIdx.x; e < a.E; e += BL_THREADS) {
+    float s = 0.f;
+    for (int q = 0; q < TEAMS; ++q) s += sm[q * (L * NV) + e];
+    part[e] = s;
+    if (a.idx) a.cpart[((long long)g * a.ctas + cta) * a.E + e] = cnt[e];
+  }
+  if (threadIdx.x == 0) a.npart[(long long)g * a.ctas + cta] = s_n;
+}
+
+__device__ __forceinline__ double block_sum(double x, double* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  double s = 0.0;
+  for (int w = 0; w < BL_JOIN / 32; ++w) s += red[w];
+  return s;
+}
+
+// One CTA per group: the CTAs' partial sums in CTA order -> usage, counts, loss, slope.
+// `sl` threads share a column when there are fewer columns than threads: slice i adds CTAs
+// i, i + sl, ..; the slices are added in order.
+__global__ void __launch_bounds__(BL_JOIN)
+balance_join_kernel(BalArgs a, int sl, int kind, float coef, float* __restrict__ loss, int32_t* __restrict__ counts,
+                    float* __restrict__ usage, float* __restrict__ slope) {
+  __shared__ double red[BL_JOIN / 32];
+  __shared__ double su[BL_JOIN];
+  __shared__ int sc[BL_JOIN];
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.x;
+  const int cols = BL_JOIN / sl;                 // columns handled at once
+  const int col = threadIdx.x % cols, slice = threadIdx.x / cols;
+  double n = 0.0;
+  for (int c = threadIdx.x; c < a.ctas; c += BL_JOIN) n += a.npart[(long long)g * a.ctas + c];
+  n = block_sum(n, red);
+  const double inv_n = n > 0.0 ? 1.0 / n : 0.0;
+  constexpr int PER = BL_MAX_E / BL_JOIN;        // columns per thread at most (sl == 1)
+  double u[PER];
+  int cc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * cols + col;
+    double s = 0.0;
+    int c = 0;
+    if (e < a.E && (i == 0 || sl == 1)) {
+      const float* part = a.part + (long long)g * a.ctas * a.E + e;
+      const int32_t* cp = a.cpart + (long long)g * a.ctas * a.E + e;
+      for (int q = slice; q < a.ctas; q += 8 * sl) {
+        float f[8];
+        int k[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const bool in = q + v * sl < a.ctas;
+          f[v] = in ? part[(long long)(q + v * sl) * a.E] : 0.f;
+          k[v] = in && a.idx ? cp[(long long)(q + v * sl) * a.E] : 0;
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          s += f[v];
+          c += k[v];
+        }
+      }
+    }
+    u[i] = s;
+    cc[i] = c;
+  }
+  if (sl > 1) {
+    su[threadIdx.x] = u[0];
+    sc[threadIdx.x] = cc[0];
+    __syncthreads();
+    if (slice == 0) {
+      for (int q = 1; q < sl; ++q) {
+        u[0] += su[q * cols + col];
+        cc[0] += sc[q * cols + col];
+      }
+    }
+  }
+  double csum = 0.0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * cols + col;
+    if (slice == 0 && e < a.E && (i == 0 || sl == 1)) csum += cc[i];
+  }
+  csum = block_sum(csum, red);
+  const double inv_c = csum > 0.0 ? 1.0 / csum : 0.0;
+  double l = 0.0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * cols + col;
+    if (slice == 0 && e < a.E && (i == 0 || sl == 1)) {
+      const double ue = u[i] * inv_n;
+      double ae;
+      if (kind == FWPKM_BALANCE_LOAD) {
+        const double f = cc[i] * inv_c;
+        l += a.E * f * ue;
+        ae = csum > 0.0 ? a.E * f - 1.0 : 0.0;
+      } else {
+        const double lg = ue > 0.0 ? log(ue) : (ue == 0.0 ? 0.0 : ue);  // NaN stays
+        l += ue * lg;
+        ae = ue > 0.0 ? lg + log((double)a.E) : (ue == 0.0 ? 0.0 : ue);
+      }
+      const long long o = (long long)g * a.E + e;
+      usage[o] = (float)ue;
+      if (counts) counts[o] = cc[i];
+      slope[o] = (float)(coef * ae * inv_n);
+    }
+  }
+  l = block_sum(l, red);
+  if (threadIdx.x == 0) loss[g] = (float)(coef * l);
+}
+
+template <typename T, int VEC, int NCH, int L>
+__global__ void __launch_bounds__(BL_THREADS)
+balance_grad_kernel(BalArgs a, const float* __restrict__ slope, const float* __restrict__ d_loss, T* __restrict__ dx) {
+  constexpr int NV = VEC * NCH;
+  constexpr int TEAMS = BL_THREADS / L;
+  __shared__ float red[BL_THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.y;
+  const int team = threadIdx.x / L, l = threadIdx.x % L;
+  const T* x = (const T*)a.x + (long long)g * a.gs;
+  const uint8_t* mask = a.mask ? a.mask + (long long)g * a.T : nullptr;
+  T* d = dx + (long long)g * a.T * a.E;
+  float s[NV];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int u = 0; u < VEC; ++u) {
+      const int e = (j * L + l) * VEC + u;
+      s[j * VEC + u] = e < a.E ? slope[(long long)g * a.E + e] : 0.f;
+    }
+  const float gl = d_loss ? d_loss[g] : 1.f;
+  const long long step = (long long)gridDim.x * TEAMS;
+  for (long long tb = (long long)blockIdx.x * TEAMS; tb < a.T; tb += step) {
+    const long long t = tb + team;
+    const bool in = t < a.T, on = in && (!mask || mask[t]);
+    float v[NV];
+    if (on) {
+      load_row<T, VEC, NCH, L>(x + t * a.ld, a.E, l, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = -INFINITY;
+    }
+    const bool live = team_softmax<NV, L>(v, red);
+    float c = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c = fmaf(v[i], s[i], c);
+    c = team_reduce<L, false>(c, red);
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int e = (j * L + l) * VEC;
+        if (e < a.E) {
+          BPack<T, VEC> p;
+#pragma unroll
+          for (int u = 0; u < VEC; ++u)
+            bal_put(p.v[u], live ? gl * v[j * VEC + u] * (s[j * VEC + u] - c) : 0.f);
+          *reinterpret_cast<BPack<T, VEC>*>(d + t * a.E + e) = p;
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+size_t b256(size_t x) { return (x + 255) / 256 * 256; }
+bool bal_al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+size_t bal_es(int dt) { return dt == FWPKM_BF16 ? 2 : 4; }
+
+// Rows per CTA of the forward: about two CTAs of BL_THREADS per SM over all groups, and at
+// least 16 rows each (a CTA costs a row of partial sums).
+void split_rows(const fwpkm_balance_config& c, int* ctas, long long* rows) {
+  long long n = (2 * 148 + c.groups - 1) / c.groups;
+  const long long most = (c.tokens + 15) / 16;
+  if (n > most) n = most;
+  if (n < 1) n = 1;
+  *rows = (c.tokens + n - 1) / n;
+  if (*rows < 1) *rows = 1;
+  *ctas = (int)((c.tokens + *rows - 1) / *rows);
+  if (*ctas < 1) *ctas = 1;
+}
+
+size_t bal_carve(const fwpkm_balance_config& c, char* base, BalArgs* a) {
+  int ctas;
+  long long rows;
+  split_rows(c, &ctas, &rows);
+  const size_t cells = (size_t)c.groups * ctas;
+  const size_t p = b256(4 * cells * c.experts);
+  if (a) {
+    a->part = (float*)base;
+    a->cpart = (int32_t*)(base + p);
+    a->npart = (int32_t*)(base + 2 * p);
+    a->ctas = ctas;
+    a->rows_cta = rows;
+  }
+  return 2 * p + b256(4 * cells);
+}
+
+fwpkm_status check_balance(const fwpkm_balance_config* c) {
+  if (!c || c->groups < 1 || c->tokens < 0 || c->experts < 1 || c->k < 0 || c->ld < c->experts || c->group_stride < 0)
+    return FWPKM_ERR_INVALID_ARG;
+  if (c->dtype != FWPKM_F32 && c->dtype != FWPKM_BF16) return FWPKM_ERR_INVALID_ARG;
+  if (c->kind != FWPKM_BALANCE_LOAD && c->kind != FWPKM_BALANCE_ENTROPY) return FWPKM_ERR_INVALID_ARG;
+  // counts are 32-bit: a group's selections must fit
+  if (c->experts > BL_MAX_E || c->groups > 65535 || c->k > BL_MAX_E ||
+      (c->k > 0 && c->tokens > 0x7fffffffLL / c->k))
+    return FWPKM_ERR_UNSUPPORTED;
+  return FWPKM_OK;
+}
+
+BalArgs bal_args(const fwpkm_balance_config& c, const void* x, const int32_t* idx, const uint8_t* mask) {
+  BalArgs a = {};
+  a.x = x; a.ld = c.ld; a.gs = c.group_stride; a.idx = idx; a.mask = mask;
+  a.G = c.groups; a.E = c.experts; a.k = c.k; a.T = c.tokens;
+  return a;
+}
+
+fwpkm_status bal_done(int launches) {
+  count_launches(launches);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return FWPKM_OK;
+  fprintf(stderr, "fwpkm: CUDA error: %s\n", cudaGetErrorString(e));
+  return FWPKM_ERR_CUDA;
+}
+
+struct BalRun {
+  bool grad;
+  BalArgs a;
+  const float* slope;
+  const float* d_loss;
+  void* dx;
+  cudaStream_t s;
+};
+
+template <typename T, int VEC, int NCH, int L>
+bool bal_go(const BalRun& r) {
+  if (!r.grad) {
+    const size_t smem = 4 * ((size_t)BL_THREADS * VEC * NCH) + (r.a.idx ? 4 * (size_t)r.a.E : 0);
+    if (smem > 48 * 1024 && !raise_smem_limit((const void*)balance_sum_kernel<T, VEC, NCH, L>, smem)) return false;
+    launch_k(balance_sum_kernel<T, VEC, NCH, L>, dim3(r.a.ctas, r.a.G), BL_THREADS, smem, r.s, r.a);
+  } else {
+    constexpr int TEAMS = BL_THREADS / L;
+    long long gx = (r.a.T + TEAMS - 1) / TEAMS;
+    const long long most = (4 * 148 + r.a.G - 1) / r.a.G;
+    if (gx > most) gx = most;
+    launch_k(balance_grad_kernel<T, VEC, NCH, L>, dim3((unsigned)gx, r.a.G), BL_THREADS, 0, r.s, r.a, r.slope,
+             r.d_loss, (T*)r.dx);
+  }
+  return true;
+}
+
+// Lanes per row: as few as hold the row in one vector each up to a warp, then more vectors
+// per lane (the row stays in registers), then the whole CTA.
+template <typename T, int VEC>
+bool bal_shape(const BalRun& r) {
+  const int v = (r.a.E + VEC - 1) / VEC;  // vectors of a row
+  if (v <= 2) return bal_go<T, VEC, 1, 2>(r);
+  if (v <= 8) return bal_go<T, VEC, 1, 8>(r);
+  if (v <= 32) return bal_go<T, VEC, 1, 32>(r);
+  if (v <= 64) return bal_go<T, VEC, 2, 32>(r);
+  if (v <= 128) return bal_go<T, VEC, 4, 32>(r);
+  if (VEC < 8 && v <= 256) return bal_go<T, VEC, 8, 32>(r);
+  if (VEC > 1) return bal_go<T, VEC, (BL_MAX_E / VEC + BL_THREADS - 1) / BL_THREADS, BL_THREADS>(r);
+  if (v <= 1024) return bal_go<T, VEC, VEC == 1 ? 32 : 1, 32>(r);
+  return bal_go<T, VEC, 8, BL_THREADS>(r);
+}
+
+template <typename T>
+bool bal_type(const BalRun& r) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  const bool vec = bal_al(r.a.x, 16) && r.a.E % VEC == 0 && r.a.ld % VEC == 0 && r.a.gs % VEC == 0 &&
+                   (!r.grad || bal_al(r.dx, 16));
+  return vec ? bal_shape<T, VEC>(r) : bal_shape<T, 1>(r);
+}
+
+}  // namespace
+}  // namespace fwpkm
+
+using namespace fwpkm;
+
+extern "C" {
+
+fwpkm_status fwpkm_balance_workspace_size(const fwpkm_balance_config* cfg, size_t* bytes) {
+  const fwpkm_status cs = check_balance(cfg);
+  if (cs != FWPKM_OK) return cs;
+  if (!bytes) return FWPKM_ERR_INVALID_ARG;
+  *bytes = bal_carve(*cfg, nullptr, nullptr);
+  return FWPKM_OK;
+}
+
+fwpkm_status fwpkm_balance_loss(const fwpkm_balance_config* cfg, const void* x, const int32_t* idx,
+                                const uint8_t* mask, void* workspace, size_t ws_bytes, float* loss, int32_t* counts,
+                                float* usage, float* slope, void* stream) {
+  NvtxRange nvtx_range("fwpkm_balance_loss");
+  const fwpkm_status cs = check_balance(cfg);
+  if (cs != FWPKM_OK) return cs;
+  if (!loss || !usage || !slope || !bal_al(loss, 4) || !bal_al(usage, 4) || !bal_al(slope, 4) ||
+      (counts && !bal_al(counts, 4)))
+    return FWPKM_ERR_INVALID_ARG;
+  if (cfg->tokens > 0 && (!x || !bal_al(x, bal_es(cfg->dtype)))) return FWPKM_ERR_INVALID_ARG;
+  if (idx && (cfg->k < 1 || !bal_al(idx, 4))) return FWPKM_ERR_INVALID_ARG;
+  if (cfg->kind == FWPKM_BALANCE_LOAD && !idx && cfg->tokens > 0) return FWPKM_ERR_INVALID_ARG;
+  if (!workspace || !bal_al(workspace, 256)) return FWPKM_ERR_INVALID_ARG;
+  if (ws_bytes < bal_carve(*cfg, nullptr, nullptr)) return FWPKM_ERR_WORKSPACE;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  BalRun r = {};
+  r.a = bal_args(*cfg, x, cfg->tokens > 0 ? idx : nullptr, mask);
+  r.s = (cudaStream_t)stream;
+  bal_carve(*cfg, (char*)workspace, &r.a);
+  const bool ok = cfg->dtype == FWPKM_BF16 ? bal_type<__nv_bfloat16>(r) : bal_type<float>(r);
+  if (!ok) return FWPKM_ERR_CUDA;
+  int sl = 1;
+  while (sl < 32 && (long long)sl * 2 * cfg->experts <= BL_JOIN && sl < r.a.ctas) sl <<= 1;
+  launch_k(balance_join_kernel, cfg->groups, BL_JOIN, 0, r.s, r.a, sl, cfg->kind, cfg->coef, loss, counts, usage,
+           slope);
+  return bal_done(2);
+}
+
+fwpkm_status fwpkm_balance_loss_backward(const fwpkm_balance_config* cfg, const void* x, const uint8_t* mask,
+                                         const float* slope, const float* d_loss, void* dx, void* stream) {
+  NvtxRange nvtx_range("fwpkm_balance_loss_backward");
+  const fwpkm_status cs = check_balance(cfg);
+  if (cs != FWPKM_OK) return cs;
+  if (cfg->tokens == 0) return FWPKM_OK;
+  const size_t es = bal_es(cfg->dtype);
+  if (!x || !slope || !dx || !bal_al(x, es) || !bal_al(dx, es) || !bal_al(slope, 4) || (d_loss && !bal_al(d_loss, 4)))
+    return FWPKM_ERR_INVALID_ARG;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  BalRun r = {};
+  r.grad = true;
+  r.a = bal_args(*cfg, x, nullptr, mask);
+  r.slope = slope;
+  r.d_loss = d_loss;
+  r.dx = dx;
+  r.s = (cudaStream_t)stream;
+  const bool ok = cfg->dtype == FWPKM_BF16 ? bal_type<__nv_bfloat16>(r) : bal_type<float>(r);
+  if (!ok) return FWPKM_ERR_CUDA;
+  return bal_done(1);
+}
+
+}  // extern "C"

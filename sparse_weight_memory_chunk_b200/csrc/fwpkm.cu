@@ -205,18 +205,25 @@ void set_carveout(const void* kern) {
 
 bool raise_smem_limit(const void* kern, size_t bytes) {
   static std::mutex mu;
-  static std::vector<std::pair<const void*, size_t>> lim;
+  struct Limit {
+    const void* kern;
+    int dev;  // the attribute is a device's own
+    size_t bytes;
+  };
+  static std::vector<Limit> lim;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
   std::lock_guard<std::mutex> lock(mu);
   for (auto& e : lim)
-    if (e.first == kern) {
-      if (bytes <= e.second) return true;
+    if (e.kern == kern && e.dev == dev) {
+      if (bytes <= e.bytes) return true;
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
         return false;
-      e.second = bytes;
+      e.bytes = bytes;
       return true;
     }
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
-  lim.emplace_back(kern, bytes);
+  lim.push_back({kern, dev, bytes});
   return true;
 }
 

@@ -1,0 +1,551 @@
+// linattn.cu -- linear attention with a decay for each head: the dense fast-weight memory
+// beside the sparse one.
+//
+// Per sequence and head, with decay a = exp(log_decay[head]) and state S [d][d_v]:
+//   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+// Gradients (D_t = dL/dS_t, D after the last token = dL/dS_T):
+//   dq_t = scale S_t do_t,   D_t = a D_{t+1} + scale q_t do_t^T  (the last token: + dS_T, undecayed),
+//   dk_t = D_t v_t,   dv_t = D_t^T k_t,   dS_0 = a D_first.
+// Each of them is the same pass with other operands: dq is the pass (q: do, k: v, v: k) from
+// S_0^T; dk the descending pass (q: v, k: do, v: q) from dS_T^T; dv the descending pass
+// (q: k, k: q, v: do) from dS_T.  So one kernel serves prompts, single tokens and training.
+//
+// This file holds the CUDA-core pass, for every type, width up to 256, stride, alignment and
+// length, and the entry points; linattn_tc.cu the tensor-core pass for bf16 prompts.
+//
+// The CUDA-core pass keeps S in fp32 registers: a CTA of 256 threads owns up to 128 columns
+// of one head's state, thread (row group, column quad) NI x 4 of its elements, and takes the
+// tokens of a batch in order: 2 FMA per state element and token.  Inside a batch of SC_TB
+// tokens the state is kept relative to the batch's start (k_u enters as a^-u k_u, o_u leaves
+// as a^u o_u), so the decay costs one multiplication per batch and its rounding does not
+// compound over the tokens; a head whose a^-SC_TB would leave fp32's range decays token by
+// token.  Bound: for single tokens the state's bytes (read and written once); for prompts
+// the FMAs.
+#include <cstdio>
+
+#include "linattn.cuh"
+
+namespace fwpkm {
+namespace {
+
+constexpr int SC_THREADS = 256;
+constexpr int SC_WARPS = SC_THREADS / 32;
+constexpr int SC_TB = 16;        // tokens per batch
+constexpr int SC_MAX_D = 256;    // rows of the state at most
+constexpr float SC_RANGE = 40.f; // largest |log a^SC_TB| kept relative to the batch
+
+__device__ __forceinline__ float sc_f(float x) { return x; }
+__device__ __forceinline__ float sc_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void sc_put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void sc_put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+template <typename T>
+__device__ __forceinline__ const T* head_row(const fwpkm_heads& x, int b, int h) {
+  return (const T*)x.p + (long long)b * x.sb + (long long)h * x.sh;
+}
+
+// local: the segment's own state from zero into its slot, no output.
+template <typename T, int NI>
+__global__ void __launch_bounds__(SC_THREADS)
+scan_kernel(ScanArgs a, int lj, int tb, int local) {
+  extern __shared__ float sm[];
+  pdl_wait();
+  pdl_trigger();
+  const int rgn = SC_THREADS / lj, dp = rgn * NI;   // row groups, padded d
+  const int cols = 4 * lj, tiles = (a.dv + cols - 1) / cols;
+  float* sk = sm;                                    // [tb][dp]
+  float* sq = sk + tb * dp;                          // [tb][dp]
+  float* sv = sq + tb * dp;                          // [tb][cols]
+  float* sr = sv + tb * cols;                        // [tb][SC_WARPS][cols] partial outputs
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int jl = tid & (lj - 1), rg = tid / lj;
+  const long long bh = blockIdx.x / tiles;
+  const int tile = (int)(blockIdx.x - bh * tiles);
+  const int b = (int)(bh / a.H), h = (int)(bh - (long long)b * a.H);
+  const int g = blockIdx.y;
+  const int c0 = tile * cols, j0 = c0 + 4 * jl, i0 = rg * NI;
+  const int n = scan_len(a, b);
+  const int t0 = min(n, g * a.seg_len), t1 = min(n, t0 + a.seg_len);
+  const float ld = a.log_decay[h];
+  const bool fast = fabsf(ld) * (float)SC_TB <= SC_RANGE;
+  const size_t cells = (size_t)a.d * a.dv;
+
+  // start state, decayed for the first token
+  float S[NI][4];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
+  if (!local) {
+    const bool slot = a.nseg > 1;
+    // segment 0 starts from the copy of s_in in the last slot, segment g from slot g - 1
+    const float* src = slot ? a.slots + ((size_t)bh * a.nseg + (g == 0 ? a.nseg - 1 : g - 1)) * cells
+                            : (a.s_in ? a.s_in + (size_t)bh * cells : nullptr);
+    if (src) {
+      const long long si = slot ? a.dv : a.si, sj = slot ? 1 : a.sj;
+      const float f = slot ? 1.f : a.in_scale;
+      const bool vec = sj == 1 && (a.dv & 3) == 0 && (((uintptr_t)src) & 15) == 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (i0 + i < a.d) {
+          if (vec) {
+            if (j0 < a.dv) {
+              const float4 x = *reinterpret_cast<const float4*>(src + (i0 + i) * si + j0);
+              S[i][0] = x.x; S[i][1] = x.y; S[i][2] = x.z; S[i][3] = x.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j0 + e < a.dv) S[i][e] = src[(i0 + i) * si + (j0 + e) * sj];
+          }
+        }
+      }
+      const float w = (t1 > t0 && !(g == 0 && a.in_ready)) ? f * decay_pow(ld, 1.f) : f;
+      if (w != 1.f) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[i][e] *= w;
+      }
+    }
+  }
+
+  const T* qp = head_row<T>(a.q, b, h);
+  const T* kp = head_row<T>(a.k, b, h);
+  const T* vp = head_row<T>(a.v, b, h);
+  T* op = (T*)a.o.p + (long long)b * a.o.sb + (long long)h * a.o.sh;
+  const float a1 = decay_pow(ld, 1.f);
+  for (int tb0 = t0; tb0 < t1; tb0 += tb) {
+    const int m = min(tb, t1 - tb0);
+    __syncthreads();
+    for (int x = tid; x < m * dp; x += SC_THREADS) {
+      const int u = x / dp, i = x - u * dp;
+      const long long t = a.reverse ? n - 1 - (tb0 + u) : tb0 + u;
+      float kv = 0.f, qv = 0.f;
+      if (i < a.d) {
+        kv = sc_f(kp[t * a.k.st + i]);
+        if (fast) kv *= decay_pow(-ld, (float)u);
+        if (!local) qv = sc_f(qp[t * a.q.st + i]);
+      }
+      sk[x] = kv;
+      if (!local) sq[x] = qv;
+    }
+    for (int x = tid; x < m * cols; x += SC_THREADS) {
+      const int u = x / cols, j = x - u * cols;
+      const long long t = a.reverse ? n - 1 - (tb0 + u) : tb0 + u;
+      sv[x] = c0 + j < a.dv ? sc_f(vp[t * a.v.st + c0 + j]) : 0.f;
+    }
+    __syncthreads();
+    const bool last = tb0 + m >= t1;
+    for (int u = 0; u < m; ++u) {
+      const float4 v4 = *reinterpret_cast<const float4*>(sv + u * cols + 4 * jl);
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      float kk[NI], qq[NI];
+      if (NI % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NI; i += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sk + u * dp + i0 + i);
+          kk[i] = x.x; kk[(i + 1) % NI] = x.y; kk[(i + 2) % NI] = x.z; kk[(i + 3) % NI] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) kk[i] = sk[u * dp + i0 + i];
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        S[i][0] = fmaf(kk[i], v4.x, S[i][0]);
+        S[i][1] = fmaf(kk[i], v4.y, S[i][1]);
+        S[i][2] = fmaf(kk[i], v4.z, S[i][2]);
+        S[i][3] = fmaf(kk[i], v4.w, S[i][3]);
+      }
+      if (!local) {
+        if (NI % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < NI; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sq + u * dp + i0 + i);
+            qq[i] = x.x; qq[(i + 1) % NI] = x.y; qq[(i + 2) % NI] = x.z; qq[(i + 3) % NI] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) qq[i] = sq[u * dp + i0 + i];
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(qq[i], S[i][e], o[e]);
+        for (int off = lj; off < 32; off <<= 1)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], off);
+        if (lane < lj)
+          *reinterpret_cast<float4*>(sr + (u * SC_WARPS + warp) * cols + 4 * jl) = make_float4(o[0], o[1], o[2], o[3]);
+      }
+      // token by token: decay for the next one (not after the segment's last)
+      if (!fast && !(last && u == m - 1)) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[i][e] *= a1;
+      }
+    }
+    if (fast) {
+      // back to absolute: a^m for the next batch's first token, a^(m-1) after the last token
+      const float e = (float)(last ? m - 1 : m);
+      const double w = exp((double)ld * e);
+      const float hi = (float)w, lo = (float)(w - (double)hi);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) S[i][x] = fmaf(S[i][x], hi, S[i][x] * lo);
+    }
+    if (!local) {
+      __syncthreads();
+      for (int x = tid; x < m * cols; x += SC_THREADS) {
+        const int u = x / cols, j = x - u * cols;
+        if (c0 + j < a.dv) {
+          float s = 0.f;
+#pragma unroll
+          for (int w = 0; w < SC_WARPS; ++w) s += sr[(u * SC_WARPS + w) * cols + j];
+          const long long t = a.reverse ? n - 1 - (tb0 + u) : tb0 + u;
+          if (fast) s *= decay_pow(ld, (float)u);
+          sc_put(op + t * a.o.st + c0 + j, s * a.out_scale);
+        }
+      }
+    }
+  }
+
+  // the segment's last state: its slot, or (last segment) the caller's
+  float* dst = local ? a.slots + ((size_t)bh * a.nseg + g) * cells
+                     : (a.s_out && g == a.nseg - 1 ? a.s_out + (size_t)bh * cells : nullptr);
+  if (!dst) return;
+  const long long si = local ? a.dv : a.si, sj = local ? 1 : a.sj;
+  const float w = local ? 1.f : a.st_scale * (a.out_decay && n > 0 ? a1 : 1.f);
+  const bool vec = sj == 1 && (a.dv & 3) == 0 && (((uintptr_t)dst) & 15) == 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    if (i0 + i >= a.d) continue;
+    if (vec) {
+      if (j0 < a.dv)
+        *reinterpret_cast<float4*>(dst + (i0 + i) * si + j0) =
+            make_float4(S[i][0] * w, S[i][1] * w, S[i][2] * w, S[i][3] * w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j0 + e < a.dv) dst[(i0 + i) * si + (j0 + e) * sj] = S[i][e] * w;
+    }
+  }
+}
+
+// Slots of local states -> states after each segment: E_g = a^len_g E_{g-1} + local_g, with
+// E_{-1} = s_in; the last slot receives a copy of s_in (in_scale applied) for segment 0.
+__global__ void __launch_bounds__(256)
+scan_combine_kernel(ScanArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t cells = (size_t)a.d * a.dv;
+  const size_t x = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= cells) return;
+  const long long bh = blockIdx.y;
+  const int b = (int)(bh / a.H), h = (int)(bh - (long long)b * a.H);
+  const int n = scan_len(a, b);
+  const float ld = a.log_decay[h];
+  const int i = (int)(x / a.dv), j = (int)(x - (size_t)i * a.dv);
+  float* slot = a.slots + (size_t)bh * a.nseg * cells + x;
+  float E = a.s_in ? a.s_in[(size_t)bh * cells + i * a.si + j * a.sj] * a.in_scale : 0.f;
+  slot[(size_t)(a.nseg - 1) * cells] = E;
+  for (int g0 = 0; g0 < a.nseg - 1; g0 += 8) {
+    float loc[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) loc[u] = g0 + u < a.nseg - 1 ? slot[(size_t)(g0 + u) * cells] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int g = g0 + u;
+      if (g >= a.nseg - 1) break;
+      const int len = max(0, min(n - g * a.seg_len, a.seg_len));
+      const int e = len - (g == 0 && a.in_ready && len > 0 ? 1 : 0);
+      const double w = e == 0 ? 1.0 : exp((double)ld * e);
+      const float hi = (float)w, lo = (float)(w - (double)hi);
+      E = fmaf(E, hi, fmaf(E, lo, loc[u]));
+      slot[(size_t)g * cells] = E;
+    }
+  }
+}
+
+bool la_al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+int pow2_ceil(int x) {
+  int p = 1;
+  while (p < x) p <<= 1;
+  return p;
+}
+
+struct ScanShape {
+  int lj, ni, tiles;
+};
+// Column quads per CTA: as wide as 16 rows per thread allow; narrower tiles when the heads
+// alone do not fill the GPU and the tokens are too few to split (each tile re-reads q and k).
+ScanShape scan_shape(const ScanArgs& a) {
+  int lj = SC_THREADS * 16 / (pow2_ceil(a.d) < 16 ? 16 : pow2_ceil(a.d));
+  if (lj > 32) lj = 32;
+  const int need = pow2_ceil((a.dv + 3) / 4);
+  if (lj > need) lj = need < 4 ? 4 : need;
+  if (a.T <= 64)
+    while (lj > 4 && (long long)a.B * a.H * ((a.dv + 4 * lj - 1) / (4 * lj)) < 148) lj >>= 1;
+  const int rg = SC_THREADS / lj;
+  int ni = 1;
+  while (ni * rg < a.d) ni <<= 1;
+  return {lj, ni, (a.dv + 4 * lj - 1) / (4 * lj)};
+}
+
+// Segments of the CUDA-core pass: one when the heads' tiles fill the GPU, else enough for
+// about two CTAs per SM, of at least 64 tokens each.
+int scan_segments(const ScanArgs& a) {
+  const long long base = (long long)a.B * a.H * scan_shape(a).tiles;
+  if (base >= 148 || a.T < 256) return 1;
+  long long n = (2 * 148 + base - 1) / base;
+  const long long most = a.T / 64;
+  if (n > most) n = most;
+  return n < 2 ? 1 : (int)n;
+}
+
+template <typename T>
+int go_scan(const ScanArgs& a, int local, cudaStream_t s) {
+  const ScanShape sh = scan_shape(a);
+  const int tb = a.T < SC_TB ? (a.T < 1 ? 1 : a.T) : SC_TB;
+  const int rg = SC_THREADS / sh.lj, dp = rg * sh.ni, cols = 4 * sh.lj;
+  const size_t smem = 4 * (size_t)tb * (2 * dp + cols + SC_WARPS * cols);
+  const dim3 grid((unsigned)((long long)a.B * a.H * sh.tiles), local ? a.nseg - 1 : a.nseg);
+#define FWPKM_SCAN(NI)                                                                           \
+  case NI:                                                                                       \
+    if (smem > 48 * 1024 && !raise_smem_limit((const void*)scan_kernel<T, NI>, smem)) return -1; \
+    launch_k(scan_kernel<T, NI>, grid, SC_THREADS, smem, s, a, sh.lj, tb, local);                 \
+    break;
+  switch (sh.ni) {
+    FWPKM_SCAN(1)
+    FWPKM_SCAN(2)
+    FWPKM_SCAN(4)
+    FWPKM_SCAN(8)
+    FWPKM_SCAN(16)
+    default: return -1;
+  }
+#undef FWPKM_SCAN
+  return 1;
+}
+
+// One pass on the CUDA cores.
+int launch_scan(ScanArgs a, int dtype, int nseg, cudaStream_t s) {
+  a.nseg = nseg;
+  a.seg_len = a.T < 1 ? 1 : a.T;
+  if (nseg > 1) a.seg_len = ((a.T + nseg - 1) / nseg + SC_TB - 1) / SC_TB * SC_TB;
+  int nl = 0;
+  auto go = [&](int local) { return dtype == FWPKM_BF16 ? go_scan<__nv_bfloat16>(a, local, s) : go_scan<float>(a, local, s); };
+  if (nseg > 1) {
+    if (go(1) < 0) return -1;
+    nl += 1 + launch_scan_combine(a, s);
+  }
+  if (go(0) < 0) return -1;
+  return nl + 1;
+}
+
+fwpkm_status check_la(const fwpkm_linattn_config* c, int T) {
+  if (!c || c->B < 1 || c->H < 1 || c->d < 1 || c->d_v < 1 || T < 0 || !(c->scale == c->scale) || c->scale == 0.f)
+    return FWPKM_ERR_INVALID_ARG;
+  if (c->dtype != FWPKM_F32 && c->dtype != FWPKM_BF16) return FWPKM_ERR_INVALID_ARG;
+  if (c->d > SC_MAX_D || c->d_v > SC_MAX_D || (long long)c->B * c->H > (1 << 24) || T > (1 << 28)) return FWPKM_ERR_UNSUPPORTED;
+  return FWPKM_OK;
+}
+
+bool heads_ok(const fwpkm_heads* x, const fwpkm_linattn_config& c, bool out, int width) {
+  if (!x || !x->p || !la_al(x->p, c.dtype == FWPKM_BF16 ? 2 : 4) || x->sb < 0 || x->sh < 0 || x->st < 0) return false;
+  // an output's rows must not share memory (inputs may be broadcast with a stride of 0)
+  if (out && (x->st < width || (c.B > 1 && x->sb == 0) || (c.H > 1 && x->sh == 0))) return false;
+  return true;
+}
+
+ScanArgs base_args(const fwpkm_linattn_config& c, int T, const float* log_decay, const int32_t* lens) {
+  ScanArgs a = {};
+  a.log_decay = log_decay; a.lens = lens;
+  a.B = c.B; a.H = c.H; a.T = T;
+  a.in_scale = 1.f; a.st_scale = 1.f;
+  return a;
+}
+ScanArgs forward_args(const fwpkm_linattn_config& c, int T, const float* log_decay, const int32_t* lens) {
+  ScanArgs a = base_args(c, T, log_decay, lens);
+  a.d = c.d; a.dv = c.d_v; a.si = c.d_v; a.sj = 1;
+  a.out_scale = c.scale;
+  return a;
+}
+
+int segments_of(const ScanArgs& a, int dtype) {
+  return scan_tc_takes(a, dtype) ? scan_tc_segments(a) : scan_segments(a);
+}
+size_t slot_bytes(const ScanArgs& a, int nseg) {
+  return nseg > 1 ? ((size_t)a.B * a.H * nseg * a.d * a.dv * 4 + 255) / 256 * 256 : 0;
+}
+int run_pass(ScanArgs a, int dtype, float* slots, cudaStream_t s) {
+  a.slots = slots;
+  if (scan_tc_takes(a, dtype)) return launch_scan_tc(a, s);
+  return launch_scan(a, dtype, scan_segments(a), s);
+}
+
+fwpkm_status la_done(int launches) {
+  if (launches > 0) count_launches(launches);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) fprintf(stderr, "fwpkm: CUDA error: %s\n", cudaGetErrorString(e));
+  return e == cudaSuccess && launches >= 0 ? FWPKM_OK : FWPKM_ERR_CUDA;
+}
+
+// Shapes of the three gradient passes.
+void grad_args(const fwpkm_linattn_config& c, int T, const float* log_decay, const int32_t* lens, ScanArgs (&p)[3]) {
+  for (int i = 0; i < 3; ++i) {
+    p[i] = base_args(c, T, log_decay, lens);
+    p[i].reverse = i > 0;
+  }
+  p[0].d = c.d_v; p[0].dv = c.d; p[0].si = 1; p[0].sj = c.d_v;   // dq: state S^T
+  p[1].d = c.d_v; p[1].dv = c.d; p[1].si = 1; p[1].sj = c.d_v;   // dk: state D^T
+  p[2].d = c.d; p[2].dv = c.d_v; p[2].si = c.d_v; p[2].sj = 1;   // dv: state D
+  p[0].out_scale = c.scale;
+  for (int i = 1; i < 3; ++i) {
+    // the pass runs on D / scale: sums of unscaled q do^T
+    p[i].out_scale = c.scale;
+    p[i].in_scale = 1.f / c.scale;
+    p[i].st_scale = c.scale;
+    p[i].in_ready = 1;
+    p[i].out_decay = 1;
+  }
+}
+
+}  // namespace
+
+int launch_scan_combine(const ScanArgs& a, cudaStream_t s) {
+  const size_t cells = (size_t)a.d * a.dv;
+  launch_k(scan_combine_kernel, dim3((unsigned)((cells + 255) / 256), (unsigned)(a.B * a.H)), 256, 0, s, a);
+  return 1;
+}
+
+}  // namespace fwpkm
+
+using namespace fwpkm;
+
+extern "C" {
+
+fwpkm_status fwpkm_linear_attention_workspace_size(const fwpkm_linattn_config* cfg, int T, int backward,
+                                                   size_t* bytes) {
+  const fwpkm_status cs = check_la(cfg, T);
+  if (cs != FWPKM_OK) return cs;
+  if (!bytes) return FWPKM_ERR_INVALID_ARG;
+  size_t most = 0;
+  if (backward) {
+    ScanArgs p[3];
+    grad_args(*cfg, T, nullptr, nullptr, p);
+    for (int i = 0; i < 3; ++i) {
+      const int cc = segments_of(p[i], cfg->dtype), gen = scan_segments(p[i]);
+      const size_t b = slot_bytes(p[i], cc > gen ? cc : gen);
+      if (b > most) most = b;
+    }
+  } else {
+    const ScanArgs a = forward_args(*cfg, T, nullptr, nullptr);
+    const int cc = segments_of(a, cfg->dtype), gen = scan_segments(a);
+    most = slot_bytes(a, cc > gen ? cc : gen);
+  }
+  *bytes = most;
+  return FWPKM_OK;
+}
+
+fwpkm_status fwpkm_linear_attention(const fwpkm_linattn_config* cfg, const fwpkm_heads* q, const fwpkm_heads* k,
+                                    const fwpkm_heads* v, int T, const float* log_decay, const int32_t* lens,
+                                    const float* s0, const fwpkm_heads* o, float* sT, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("fwpkm_linear_attention");
+  const fwpkm_status cs = check_la(cfg, T);
+  if (cs != FWPKM_OK) return cs;
+  if (!log_decay || !la_al(log_decay, 4) || (lens && !la_al(lens, 4)) || (s0 && !la_al(s0, 4)) || (sT && !la_al(sT, 4)))
+    return FWPKM_ERR_INVALID_ARG;
+  ScanArgs a = forward_args(*cfg, T, log_decay, lens);
+  if (T > 0) {
+    if (!heads_ok(q, *cfg, false, cfg->d) || !heads_ok(k, *cfg, false, cfg->d) || !heads_ok(v, *cfg, false, cfg->d_v) ||
+        !heads_ok(o, *cfg, true, cfg->d_v))
+      return FWPKM_ERR_INVALID_ARG;
+    a.q = *q; a.k = *k; a.v = *v; a.o = *o;
+  } else if (!sT) {
+    return FWPKM_OK;
+  }
+  a.s_in = s0;
+  a.s_out = sT;
+  size_t need = 0;
+  fwpkm_linear_attention_workspace_size(cfg, T, 0, &need);
+  if (need > 0 && (!workspace || !la_al(workspace, 256))) return FWPKM_ERR_INVALID_ARG;
+  if (ws_bytes < need) return FWPKM_ERR_WORKSPACE;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  return la_done(run_pass(a, cfg->dtype, (float*)workspace, (cudaStream_t)stream));
+}
+
+fwpkm_status fwpkm_linear_attention_backward(const fwpkm_linattn_config* cfg, const fwpkm_heads* q,
+                                             const fwpkm_heads* k, const fwpkm_heads* v, int T,
+                                             const float* log_decay, const int32_t* lens, const float* s0,
+                                             const fwpkm_heads* d_o, const float* d_sT, const fwpkm_heads* dq,
+                                             const fwpkm_heads* dk, const fwpkm_heads* dv, float* ds0,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("fwpkm_linear_attention_backward");
+  const fwpkm_status cs = check_la(cfg, T);
+  if (cs != FWPKM_OK) return cs;
+  if (!log_decay || !la_al(log_decay, 4) || (lens && !la_al(lens, 4)) || (s0 && !la_al(s0, 4)) ||
+      (d_sT && !la_al(d_sT, 4)) || (ds0 && !la_al(ds0, 4)))
+    return FWPKM_ERR_INVALID_ARG;
+  ScanArgs p[3];
+  grad_args(*cfg, T, log_decay, lens, p);
+  if (T > 0) {
+    if (!heads_ok(q, *cfg, false, cfg->d) || !heads_ok(k, *cfg, false, cfg->d) || !heads_ok(v, *cfg, false, cfg->d_v) ||
+        !heads_ok(d_o, *cfg, false, cfg->d_v) || !heads_ok(dq, *cfg, true, cfg->d) ||
+        !heads_ok(dk, *cfg, true, cfg->d) || !heads_ok(dv, *cfg, true, cfg->d_v))
+      return FWPKM_ERR_INVALID_ARG;
+    p[0].q = *d_o; p[0].k = *v; p[0].v = *k; p[0].o = *dq;
+    p[1].q = *v; p[1].k = *d_o; p[1].v = *q; p[1].o = *dk;
+    p[2].q = *k; p[2].k = *q; p[2].v = *d_o; p[2].o = *dv;
+  }
+  p[0].s_in = s0;
+  p[1].s_in = d_sT;
+  p[2].s_in = d_sT;
+  p[2].s_out = ds0;
+  if (T == 0 && !ds0) return FWPKM_OK;
+  size_t need = 0;
+  fwpkm_linear_attention_workspace_size(cfg, T, 1, &need);
+  if (need > 0 && (!workspace || !la_al(workspace, 256))) return FWPKM_ERR_INVALID_ARG;
+  if (ws_bytes < need) return FWPKM_ERR_WORKSPACE;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  int nl = 0;
+  // dv last: it alone writes ds0, which may be d_sT's own memory
+  for (int i = T > 0 ? 0 : 2; i < 3; ++i) {
+    const int r = run_pass(p[i], cfg->dtype, (float*)workspace, (cudaStream_t)stream);
+    if (r < 0) return la_done(-1);
+    nl += r;
+  }
+  return la_done(nl);
+}
+
+fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const fwpkm_heads* q, const fwpkm_heads* k,
+                                         const fwpkm_heads* v, int n_tok, const float* log_decay,
+                                         const int32_t* lens, const float* state, const fwpkm_heads* o,
+                                         float* state_out, void* stream) {
+  NvtxRange nvtx_range("fwpkm_linear_attention_step");
+  const fwpkm_status cs = check_la(cfg, n_tok);
+  if (cs != FWPKM_OK) return cs;
+  if (!log_decay || !la_al(log_decay, 4) || (lens && !la_al(lens, 4)) || !state || !state_out || !la_al(state, 4) ||
+      !la_al(state_out, 4))
+    return FWPKM_ERR_INVALID_ARG;
+  if (n_tok == 0 && state == state_out) return FWPKM_OK;
+  ScanArgs a = forward_args(*cfg, n_tok, log_decay, lens);
+  if (n_tok > 0) {
+    if (!heads_ok(q, *cfg, false, cfg->d) || !heads_ok(k, *cfg, false, cfg->d) || !heads_ok(v, *cfg, false, cfg->d_v) ||
+        !heads_ok(o, *cfg, true, cfg->d_v))
+      return FWPKM_ERR_INVALID_ARG;
+    a.q = *q; a.k = *k; a.v = *v; a.o = *o;
+  }
+  a.s_in = state;
+  a.s_out = state_out;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  return la_done(launch_scan(a, cfg->dtype, 1, (cudaStream_t)stream));
+}
+
+}  // extern "C"

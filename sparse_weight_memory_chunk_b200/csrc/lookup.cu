@@ -1,0 +1,912 @@
+// lookup.cu -- weighted lookups of a learned table and their gradients.
+//
+//   out_t    = scale * sum_r w[t,r] table[idx[t,r]]            (r < R; w absent: ones)
+//   dtable_i = scale * sum_{(t,r): idx[t,r] = i} w[t,r] dout_t
+//   dw[t,r]  = scale * <dout_t, table[idx[t,r]]>
+//
+// With R = 1 and no w this is a token embedding; with the slots and weights of a
+// product-key selection it is the read of a slow value table.  Entries outside [0, rows)
+// contribute nothing (their dw is 0).
+//
+// All three are bound by HBM: the forward reads every used row once and writes out once; the
+// gradient reads dout once per pair and writes (or updates) every row of dtable once.
+// No float atomics: the (row, pair) list is sorted by row with a stable radix sort, so each
+// row's terms are summed in pair order and the results are deterministic.
+#include <cstdio>
+
+#include "fwpkm_internal.cuh"
+
+namespace fwpkm {
+namespace {
+
+constexpr int LK_THREADS = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// VEC consecutive elements as one load or store (VEC * sizeof(T) = 16 bytes, or one element).
+template <typename T, int VEC>
+struct __align__(sizeof(T) * VEC) Pack {
+  T v[VEC];
+};
+
+template <typename I>
+__device__ __forceinline__ long long load_idx(const I* p, long long i) { return (long long)__ldg(p + i); }
+
+// Threads across a row's vectors (a power of two) for a row of `vecs` vectors.
+int row_threads(long long vecs) {
+  int t = 1;
+  while (t < LK_THREADS && t < vecs) t <<= 1;
+  return t;
+}
+
+// One thread per vector of an output row, TU tokens per thread: their indices, then their
+// rows, are in flight together.
+template <typename T, typename I, int VEC, int TU>
+__global__ void __launch_bounds__(LK_THREADS)
+lookup_row_kernel(const T* __restrict__ table, long long rows, long long ld, const I* __restrict__ idx,
+                  const float* __restrict__ w, long long n, int vecs, int tx_n, float scale, T* __restrict__ out,
+                  long long out_ld) {
+  pdl_wait();
+  pdl_trigger();
+  const int ty_n = LK_THREADS / tx_n;
+  const int tx = threadIdx.x & (tx_n - 1), ty = threadIdx.x / tx_n;
+  const int c = blockIdx.y * tx_n + tx;
+  if (c >= vecs) return;
+  const long long t0 = (long long)blockIdx.x * ty_n * TU + ty;
+  long long row[TU];
+  Pack<T, VEC> x[TU];
+#pragma unroll
+  for (int u = 0; u < TU; ++u) {
+    const long long t = t0 + (long long)u * ty_n;
+    row[u] = t < n ? load_idx(idx, t) : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < TU; ++u)
+    if (row[u] >= 0 && row[u] < rows)
+      x[u] = *reinterpret_cast<const Pack<T, VEC>*>(table + row[u] * ld + (long long)c * VEC);
+#pragma unroll
+  for (int u = 0; u < TU; ++u) {
+    const long long t = t0 + (long long)u * ty_n;
+    if (t >= n) return;
+    const bool ok = row[u] >= 0 && row[u] < rows;
+    const float f = w ? __ldg(w + t) * scale : scale;
+    Pack<T, VEC> y;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) y.v[e] = from_f<T>(ok ? to_f<T>(x[u].v[e]) * f : 0.f);
+    *reinterpret_cast<Pack<T, VEC>*>(out + t * out_ld + (long long)c * VEC) = y;
+  }
+}
+
+// One thread per vector of an output row; the bag's rows four at a time, added in rank order.
+template <typename T, typename I, int VEC>
+__global__ void __launch_bounds__(LK_THREADS)
+lookup_bag_kernel(const T* __restrict__ table, long long rows, long long ld, const I* __restrict__ idx,
+                  const float* __restrict__ w, long long n, int R, int vecs, int tx_n, float scale,
+                  T* __restrict__ out, long long out_ld) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int U = 4;
+  const int ty_n = LK_THREADS / tx_n;
+  const int tx = threadIdx.x & (tx_n - 1), ty = threadIdx.x / tx_n;
+  const int c = blockIdx.y * tx_n + tx;
+  const long long t = (long long)blockIdx.x * ty_n + ty;
+  if (c >= vecs || t >= n) return;
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  for (int r0 = 0; r0 < R; r0 += U) {
+    long long row[U];
+    float f[U];
+    Pack<T, VEC> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      row[u] = r0 + u < R ? load_idx(idx, t * R + r0 + u) : -1;
+      if (row[u] >= rows) row[u] = -1;
+      f[u] = row[u] >= 0 ? (w ? __ldg(w + t * R + r0 + u) : 1.f) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (row[u] >= 0) x[u] = *reinterpret_cast<const Pack<T, VEC>*>(table + row[u] * ld + (long long)c * VEC);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (row[u] >= 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f[u], to_f<T>(x[u].v[e]), acc[e]);
+      }
+  }
+  Pack<T, VEC> y;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) y.v[e] = from_f<T>(acc[e] * scale);
+  *reinterpret_cast<Pack<T, VEC>*>(out + t * out_ld + (long long)c * VEC) = y;
+}
+
+// dw: one warp per (token, DW_U ranks): the token's dout vectors are loaded once for them.
+constexpr int DW_U = 4;
+template <typename T, typename I, int VEC>
+__global__ void __launch_bounds__(LK_THREADS)
+lookup_dw_kernel(const T* __restrict__ table, long long rows, long long ld, const I* __restrict__ idx,
+                 const T* __restrict__ d_out, long long out_ld, long long n, int R, int vecs, float scale,
+                 float* __restrict__ dw) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int groups = (R + DW_U - 1) / DW_U;
+  const long long job = (long long)blockIdx.x * (LK_THREADS / 32) + (threadIdx.x >> 5);
+  const long long t = job / groups;
+  if (t >= n) return;
+  const int r0 = (int)(job - t * groups) * DW_U;
+  long long row[DW_U];
+  float acc[DW_U];
+#pragma unroll
+  for (int u = 0; u < DW_U; ++u) {
+    row[u] = r0 + u < R ? load_idx(idx, t * R + r0 + u) : -1;
+    if (row[u] >= rows) row[u] = -1;
+    acc[u] = 0.f;
+  }
+  for (int c = lane; c < vecs; c += 32) {
+    const Pack<T, VEC> g = *reinterpret_cast<const Pack<T, VEC>*>(d_out + t * out_ld + (long long)c * VEC);
+    Pack<T, VEC> x[DW_U];
+#pragma unroll
+    for (int u = 0; u < DW_U; ++u)
+      if (row[u] >= 0) x[u] = *reinterpret_cast<const Pack<T, VEC>*>(table + row[u] * ld + (long long)c * VEC);
+#pragma unroll
+    for (int u = 0; u < DW_U; ++u)
+      if (row[u] >= 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[u] = fmaf(to_f<T>(g.v[e]), to_f<T>(x[u].v[e]), acc[u]);
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < DW_U; ++u) acc[u] = warp_sum(acc[u]);
+  if (lane == 0) {
+#pragma unroll
+    for (int u = 0; u < DW_U; ++u)
+      if (r0 + u < R) dw[t * R + r0 + u] = row[u] >= 0 ? acc[u] * scale : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Stable radix sort of the pairs by row.  Key: the row, or `rows` for an entry outside the
+// table (sorted last and dropped).  Payload: the pair's index.  Least significant digit
+// first, one counting pass per digit of up to RS_BITS bits.
+// ---------------------------------------------------------------------------
+constexpr int RS_THREADS = 512;
+constexpr int RS_WARPS = RS_THREADS / 32;
+constexpr int RS_BITS = 11;                 // 2048 bins: two passes up to 2^22 rows
+constexpr int RS_MAX_BINS = 1 << RS_BITS;
+constexpr int RS_ITEMS = 8;                 // items per thread of a tile
+constexpr int RS_TILE = RS_THREADS * RS_ITEMS;
+// Up to this many tiles every scatter CTA forms its own offsets from the tiles' counts;
+// beyond it a scan launch does (the counts read by all CTAs grow with tiles^2).
+constexpr int RS_OWN_SCAN = 32;
+
+template <typename I>
+__device__ __forceinline__ uint32_t pair_key(const I* idx, long long p, long long rows) {
+  const long long r = load_idx(idx, p);
+  return r >= 0 && r < rows ? (uint32_t)r : (uint32_t)rows;
+}
+
+// Where a pass reads its keys: the indices themselves (first pass) or the previous pass.
+template <typename I>
+struct Source {
+  const I* idx;
+  const uint32_t* key;
+  const uint32_t* pos;
+  long long rows;
+  __device__ __forceinline__ uint32_t k(long long p) const { return key ? key[p] : pair_key(idx, p, rows); }
+  __device__ __forceinline__ uint32_t v(long long p) const { return key ? pos[p] : (uint32_t)p; }
+};
+
+// Counts of one tile's digits: hist[tile][bin].
+template <typename I>
+__global__ void __launch_bounds__(RS_THREADS)
+sort_hist_kernel(Source<I> src, long long P, int shift, int bins, uint32_t* __restrict__ hist) {
+  __shared__ uint32_t s[RS_MAX_BINS];
+  pdl_wait();
+  pdl_trigger();
+  for (int b = threadIdx.x; b < bins; b += RS_THREADS) s[b] = 0u;
+  __syncthreads();
+  const long long base = (long long)blockIdx.x * RS_TILE;
+#pragma unroll
+  for (int i = 0; i < RS_ITEMS; ++i) {
+    const long long p = base + i * RS_THREADS + threadIdx.x;
+    if (p < P) atomicAdd(&s[(src.k(p) >> shift) & (bins - 1)], 1u);
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += RS_THREADS) hist[(long long)blockIdx.x * bins + b] = s[b];
+}
+
+// hist[tile][bin] -> its exclusive sum over the tiles; total[bin] = the bin's count.
+__global__ void __launch_bounds__(128)
+sort_scan_kernel(uint32_t* __restrict__ hist, uint32_t* __restrict__ total, int tiles, int bins) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x * 128 + threadIdx.x;
+  if (b >= bins) return;
+  uint32_t run = 0;
+  for (int t0 = 0; t0 < tiles; t0 += 16) {
+    uint32_t x[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) x[u] = t0 + u < tiles ? hist[(long long)(t0 + u) * bins + b] : 0u;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      if (t0 + u < tiles) {
+        hist[(long long)(t0 + u) * bins + b] = run;
+        run += x[u];
+      }
+  }
+  total[b] = run;
+}
+
+// Exclusive sum over `bins` values in shared memory (bins <= RS_MAX_BINS, RS_THREADS threads).
+__device__ __forceinline__ void block_exclusive(uint32_t* s, int bins, uint32_t* warp_tot) {
+  constexpr int PER = RS_MAX_BINS / RS_THREADS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = threadIdx.x * PER + i;
+    x[i] = b < bins ? s[b] : 0u;
+    sum += x[i];
+  }
+  uint32_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_tot[warp] = inc;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_tot[w];
+  uint32_t run = before + inc - sum;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = threadIdx.x * PER + i;
+    if (b < bins) s[b] = run;
+    run += x[i];
+  }
+  __syncthreads();
+}
+
+// Stable ranks of a tile's items inside their bins: warp w holds items [w, w+1) * 32 RS_ITEMS
+// of the tile in order, 32 at a time; lanes with equal digits rank each other by lane.
+// wh[warp][bin] (uint16) ends as the number of earlier items of the tile in the bin from
+// earlier warps; rank[i] counts those of the same warp.
+__device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[RS_ITEMS], const bool (&live)[RS_ITEMS],
+                                           uint16_t* wh, int bins, uint32_t (&rank)[RS_ITEMS]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = threadIdx.x; b < bins * RS_WARPS / 2; b += RS_THREADS) reinterpret_cast<uint32_t*>(wh)[b] = 0u;
+  __syncthreads();
+  uint16_t* mine = wh + (size_t)warp * bins;
+#pragma unroll
+  for (int i = 0; i < RS_ITEMS; ++i) {
+    const uint32_t d = live[i] ? digit[i] : 0xffffffffu;
+    const unsigned peers = __match_any_sync(0xffffffffu, d);
+    const unsigned below = __popc(peers & ((1u << lane) - 1u));
+    uint32_t old = 0;
+    if (live[i]) old = mine[digit[i]];
+    __syncwarp();
+    if (live[i] && below == 0) mine[digit[i]] = (uint16_t)(old + __popc(peers));
+    __syncwarp();
+    rank[i] = old + below;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += RS_THREADS) {
+    uint32_t run = 0;
+#pragma unroll
+    for (int w = 0; w < RS_WARPS; ++w) {
+      const uint32_t c = wh[(size_t)w * bins + b];
+      wh[(size_t)w * bins + b] = (uint16_t)run;
+      run += c;
+    }
+  }
+  __syncthreads();
+}
+
+// Scatter one tile to its sorted places.  own_scan: hist holds plain counts and this CTA
+// forms its offsets (tiles <= RS_OWN_SCAN); else hist is already the exclusive sum over tiles.
+template <typename I>
+__global__ void __launch_bounds__(RS_THREADS)
+sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint32_t* __restrict__ hist,
+                    const uint32_t* __restrict__ total, int tiles, int own_scan, uint32_t* __restrict__ key_out,
+                    uint32_t* __restrict__ pos_out) {
+  extern __shared__ uint32_t sm[];
+  uint32_t* base = sm;                              // [bins]
+  uint32_t* before = sm + bins;                     // [bins] earlier tiles' items of the bin
+  uint16_t* wh = (uint16_t*)(sm + 2 * bins);        // [RS_WARPS][bins]
+  __shared__ uint32_t warp_tot[RS_WARPS];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile = blockIdx.x;
+  uint32_t key[RS_ITEMS], pos[RS_ITEMS], digit[RS_ITEMS], rank[RS_ITEMS];
+  bool live[RS_ITEMS];
+#pragma unroll
+  for (int i = 0; i < RS_ITEMS; ++i) {
+    const long long p = (long long)tile * RS_TILE + (warp * RS_ITEMS + i) * 32 + lane;
+    live[i] = p < P;
+    key[i] = live[i] ? src.k(p) : 0u;
+    pos[i] = live[i] ? src.v(p) : 0u;
+    digit[i] = (key[i] >> shift) & (bins - 1);
+  }
+  for (int b = threadIdx.x; b < bins; b += RS_THREADS) {
+    uint32_t tot = 0, bef = 0;
+    if (own_scan) {
+      for (int t = 0; t < tiles; ++t) {
+        const uint32_t c = hist[(long long)t * bins + b];
+        if (t == tile) bef = tot;
+        tot += c;
+      }
+    } else {
+      tot = total[b];
+      bef = hist[(long long)tile * bins + b];
+    }
+    base[b] = tot;
+    before[b] = bef;
+  }
+  __syncthreads();
+  block_exclusive(base, bins, warp_tot);
+  tile_ranks(digit, live, wh, bins, rank);
+#pragma unroll
+  for (int i = 0; i < RS_ITEMS; ++i)
+    if (live[i]) {
+      const uint32_t d = digit[i];
+      const uint32_t at = base[d] + before[d] + wh[(size_t)warp * bins + d] + rank[i];
+      key_out[at] = key[i];
+      pos_out[at] = pos[i];
+    }
+}
+
+// Up to one tile of pairs: the whole sort in one CTA, the passes through shared memory.
+template <typename I>
+__global__ void __launch_bounds__(RS_THREADS)
+sort_small_kernel(const I* __restrict__ idx, int P, long long rows, int bits, int passes,
+                  uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out) {
+  extern __shared__ uint32_t sm[];
+  const int per = (bits + passes - 1) / passes, bins = 1 << per;
+  uint32_t* sk = sm;                                // [RS_TILE]
+  uint32_t* sp = sm + RS_TILE;                      // [RS_TILE]
+  uint32_t* base = sp + RS_TILE;                    // [bins]
+  uint16_t* wh = (uint16_t*)(base + bins);          // [RS_WARPS][bins]
+  __shared__ uint32_t warp_tot[RS_WARPS];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t key[RS_ITEMS], pos[RS_ITEMS], digit[RS_ITEMS], rank[RS_ITEMS];
+  bool live[RS_ITEMS];
+#pragma unroll
+  for (int i = 0; i < RS_ITEMS; ++i) {
+    const int p = (warp * RS_ITEMS + i) * 32 + lane;
+    live[i] = p < P;
+    key[i] = live[i] ? pair_key(idx, p, rows) : 0u;
+    pos[i] = (uint32_t)p;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int b = threadIdx.x; b < bins; b += RS_THREADS) base[b] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RS_ITEMS; ++i) {
+      digit[i] = (key[i] >> (pass * per)) & (bins - 1);
+      if (live[i]) atomicAdd(&base[digit[i]], 1u);
+    }
+    __syncthreads();
+    block_exclusive(base, bins, warp_tot);
+    tile_ranks(digit, live, wh, bins, rank);
+    const bool last = pass == passes - 1;
+#pragma unroll
+    for (int i = 0; i < RS_ITEMS; ++i)
+      if (live[i]) {
+        const uint32_t at = base[digit[i]] + wh[(size_t)warp * bins + digit[i]] + rank[i];
+        (last ? key_out : sk)[at] = key[i];
+        (last ? pos_out : sp)[at] = pos[i];
+      }
+    __syncthreads();
+    if (!last) {
+#pragma unroll
+      for (int i = 0; i < RS_ITEMS; ++i) {
+        const int p = (warp * RS_ITEMS + i) * 32 + lane;
+        if (live[i]) {
+          key[i] = sk[p];
+          pos[i] = sp[p];
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Segmented sum of the sorted pairs.  A team of tx_n threads (one vector of columns each)
+// owns SEG consecutive sorted pairs.  A row whose pairs lie inside the range is written at
+// once; a row cut by the range's ends leaves a partial sum, and the second launch adds a
+// cut row's partials in order.  SEG = 32 bounds the serial work on a row that everything
+// reads to SEG terms plus its partials.
+// ---------------------------------------------------------------------------
+constexpr int SEG = 32;
+constexpr int SEG_U = 8;  // pairs in flight per team
+
+struct SegArgs {
+  const uint32_t* key;
+  const uint32_t* pos;
+  const float* w;
+  long long P, rows, out_ld, grad_ld;
+  int R, vecs, tx_n, width;
+  float scale;
+  int accumulate;
+  float* part;        // [ranges][2][width] fp32: the sums cut at the range's start and end
+  long long ranges;
+};
+
+template <typename G, int VEC>
+__device__ __forceinline__ void put_row(G* d_table, const SegArgs& a, uint32_t row, int c, const float (&acc)[VEC]) {
+  G* dst = d_table + (long long)row * a.grad_ld + (long long)c * VEC;
+  constexpr int GV = (sizeof(G) * VEC > 16) ? 16 / (int)sizeof(G) : VEC;  // elements per 16-byte access
+#pragma unroll
+  for (int h = 0; h < VEC / GV; ++h) {
+    Pack<G, GV> y;
+    if (a.accumulate) y = *reinterpret_cast<const Pack<G, GV>*>(dst + h * GV);
+#pragma unroll
+    for (int e = 0; e < GV; ++e) {
+      const float s = acc[h * GV + e] * a.scale;
+      y.v[e] = from_f<G>(a.accumulate ? to_f<G>(y.v[e]) + s : s);
+    }
+    *reinterpret_cast<Pack<G, GV>*>(dst + h * GV) = y;
+  }
+}
+
+// Whether `row` occurs in the sorted keys.
+__device__ __forceinline__ bool has_row(const uint32_t* __restrict__ key, long long P, uint32_t row) {
+  long long lo = 0, hi = P;
+  while (lo < hi) {
+    const long long mid = (lo + hi) >> 1;
+    if (__ldg(key + mid) < row) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo < P && __ldg(key + lo) == row;
+}
+
+template <typename T, typename G, int VEC>
+__global__ void __launch_bounds__(LK_THREADS)
+lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_table, int sum_blocks) {
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x >= sum_blocks) {
+    // ---- rows no pair reads: zero (dense gradient only).  A warp takes 32 rows, each lane
+    // looks one of them up in the sorted keys, then the warp writes the missing ones.
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)(gridDim.x - sum_blocks) * (LK_THREADS / 32);
+    const long long w0 = (long long)(blockIdx.x - sum_blocks) * (LK_THREADS / 32) + (threadIdx.x >> 5);
+    for (long long r0 = w0 * 32; r0 < a.rows; r0 += warps * 32) {
+      const long long r = r0 + lane;
+      const bool zero = r < a.rows && !has_row(a.key, a.P, (uint32_t)r);
+      unsigned todo = __ballot_sync(0xffffffffu, zero);
+      while (todo) {
+        const int l = __ffs(todo) - 1;
+        todo &= todo - 1;
+        G* dst = d_table + (r0 + l) * a.grad_ld;
+        constexpr int GV = VEC == 1 ? 1 : 16 / (int)sizeof(G);
+        Pack<G, GV> z;
+#pragma unroll
+        for (int e = 0; e < GV; ++e) z.v[e] = from_f<G>(0.f);
+        for (int c = lane; c < a.width / GV; c += 32) *reinterpret_cast<Pack<G, GV>*>(dst + (long long)c * GV) = z;
+      }
+    }
+    return;
+  }
+  const int ty_n = LK_THREADS / a.tx_n;
+  const int tx = threadIdx.x & (a.tx_n - 1), ty = threadIdx.x / a.tx_n;
+  const int c = blockIdx.y * a.tx_n + tx;
+  const long long range = (long long)blockIdx.x * ty_n + ty;
+  if (c >= a.vecs || range >= a.ranges) return;
+  const long long p0 = range * SEG, p1 = p0 + SEG < a.P ? p0 + SEG : a.P;
+  const uint32_t none = (uint32_t)a.rows;
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  uint32_t cur = a.key[p0];
+  const bool cut_start = p0 > 0 && a.key[p0 - 1] == cur;
+  const bool cut_end = p1 < a.P && a.key[p1] == a.key[p1 - 1];
+  bool first = true;  // still in the range's first row
+  for (long long q0 = p0; q0 < p1; q0 += SEG_U) {
+    uint32_t k[SEG_U];
+    float f[SEG_U];
+    Pack<T, VEC> x[SEG_U];
+#pragma unroll
+    for (int u = 0; u < SEG_U; ++u) {
+      const long long p = q0 + u;
+      k[u] = p < p1 ? a.key[p] : none;
+      f[u] = 0.f;
+      if (k[u] != none) {
+        const uint32_t pr = a.pos[p];
+        f[u] = a.w ? __ldg(a.w + pr) : 1.f;
+        x[u] = *reinterpret_cast<const Pack<T, VEC>*>(d_out + (long long)(pr / a.R) * a.out_ld + (long long)c * VEC);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < SEG_U; ++u) {
+      if (q0 + u < p1) {
+        if (k[u] != cur) {
+          if (cur != none) {
+            if (first && cut_start) {
+              float* d = a.part + (range * 2) * a.width + (long long)c * VEC;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) d[e] = acc[e];
+            } else {
+              put_row<G, VEC>(d_table, a, cur, c, acc);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+          cur = k[u];
+          first = false;
+        }
+        if (cur != none) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f[u], to_f<T>(x[u].v[e]), acc[e]);
+        }
+      }
+    }
+  }
+  if (cur == none) return;
+  if ((first && cut_start) || cut_end) {
+    // a row cut at both ends is one partial, kept as the start's
+    float* d = a.part + (range * 2 + ((first && cut_start) ? 0 : 1)) * a.width + (long long)c * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) d[e] = acc[e];
+  } else {
+    put_row<G, VEC>(d_table, a, cur, c, acc);
+  }
+}
+
+// Rows cut by range ends: the team of the range where the row begins adds its partials.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(LK_THREADS)
+lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
+  pdl_wait();
+  pdl_trigger();
+  const int ty_n = LK_THREADS / a.tx_n;
+  const int tx = threadIdx.x & (a.tx_n - 1), ty = threadIdx.x / a.tx_n;
+  const int c = blockIdx.y * a.tx_n + tx;
+  const long long range = (long long)blockIdx.x * ty_n + ty;
+  if (c >= a.vecs || range + 1 >= a.ranges) return;
+  const long long p0 = range * SEG, p1 = p0 + SEG;  // not the last range: full
+  const uint32_t row = a.key[p1 - 1];
+  if (row == (uint32_t)a.rows || a.key[p1] != row) return;     // nothing cut at the end
+  if (a.key[p0] == row && p0 > 0 && a.key[p0 - 1] == row) return;  // the row began earlier
+  // last range that holds the row: the ranges after this one whose first key is the row
+  long long lo = range + 1, hi = a.ranges;
+  while (lo < hi) {
+    const long long mid = (lo + hi) >> 1;
+    if (a.key[mid * SEG] == row) lo = mid + 1;
+    else hi = mid;
+  }
+  float acc[VEC];
+  const float* d = a.part + (range * 2 + 1) * a.width + (long long)c * VEC;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = d[e];
+  for (long long q0 = range + 1; q0 < lo; q0 += 8) {
+    float x[8][VEC];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        x[u][e] = q0 + u < lo ? a.part[((q0 + u) * 2) * a.width + (long long)c * VEC + e] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] += x[u][e];
+  }
+  put_row<G, VEC>(d_table, a, row, c, acc);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+bool ptr_al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+size_t dsize(int dt) { return dt == FWPKM_BF16 ? 2 : 4; }
+
+int key_bits(long long rows) {  // bits of the largest key, `rows`
+  int b = 1;
+  while (b < 32 && (rows >> b) != 0) ++b;
+  return b;
+}
+
+struct SortPlan {
+  int bits, passes, per, bins, tiles;
+};
+SortPlan sort_plan(long long rows, long long P) {
+  SortPlan s;
+  s.bits = key_bits(rows);
+  s.passes = (s.bits + RS_BITS - 1) / RS_BITS;
+  s.per = (s.bits + s.passes - 1) / s.passes;
+  s.bins = 1 << s.per;
+  s.tiles = (int)((P + RS_TILE - 1) / RS_TILE);
+  return s;
+}
+
+struct BackWork {
+  uint32_t *key[2], *pos[2], *hist, *total;
+  float* part;
+};
+size_t back_carve(const fwpkm_lookup_config& c, long long P, char* base, BackWork* w) {
+  const SortPlan sp = sort_plan(c.rows, P);
+  const long long ranges = (P + SEG - 1) / SEG;
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> char* {
+    char* p = base ? base + off : nullptr;
+    off += up256(bytes);
+    return p;
+  };
+  BackWork b;
+  for (int i = 0; i < 2; ++i) {
+    b.key[i] = (uint32_t*)take(4 * (size_t)P);
+    b.pos[i] = (uint32_t*)take(4 * (size_t)P);
+  }
+  b.hist = (uint32_t*)take(4 * (size_t)sp.tiles * sp.bins);
+  b.total = (uint32_t*)take(4 * (size_t)sp.bins);
+  b.part = (float*)take(4 * 2 * (size_t)ranges * c.width);
+  if (w) *w = b;
+  return off;
+}
+
+fwpkm_status check_lookup(const fwpkm_lookup_config* c, long long n) {
+  if (!c || n < 0 || c->rows < 1 || c->width < 1 || c->R < 1 || c->table_ld < c->width || c->out_ld < c->width)
+    return FWPKM_ERR_INVALID_ARG;
+  if (c->dtype != FWPKM_F32 && c->dtype != FWPKM_BF16) return FWPKM_ERR_INVALID_ARG;
+  if (c->idx_dtype != FWPKM_I32 && c->idx_dtype != FWPKM_I64) return FWPKM_ERR_INVALID_ARG;
+  if (c->rows > 0x7ffffffeLL || c->width > (1 << 20) || c->R > 1024 || n > 0x7fffffffLL / c->R)
+    return FWPKM_ERR_UNSUPPORTED;
+  return FWPKM_OK;
+}
+
+fwpkm_status done(int launches) {
+  count_launches(launches);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return FWPKM_OK;
+  fprintf(stderr, "fwpkm: CUDA error: %s\n", cudaGetErrorString(e));
+  return FWPKM_ERR_CUDA;
+}
+
+// Rows are taken 16 bytes at a time when every row starts on a 16-byte boundary and holds
+// whole vectors; one element at a time otherwise (any width, stride or alignment).
+template <typename T>
+bool rows_vec(const void* p, long long ld, int width) {
+  return ptr_al(p, 16) && (ld * sizeof(T)) % 16 == 0 && (width * sizeof(T)) % 16 == 0;
+}
+
+template <typename T, typename I, int VEC>
+void go_lookup(const fwpkm_lookup_config& c, const void* table, const void* idx, const float* w, long long n,
+               void* out, cudaStream_t s) {
+  const int vecs = c.width / VEC, tx = row_threads(vecs), ty = LK_THREADS / tx;
+  const unsigned gy = (unsigned)((vecs + tx - 1) / tx);
+  if (c.R == 1) {
+    constexpr int TU = 2;
+    const unsigned gx = (unsigned)((n + (long long)ty * TU - 1) / ((long long)ty * TU));
+    launch_k(lookup_row_kernel<T, I, VEC, TU>, dim3(gx, gy), LK_THREADS, 0, s, (const T*)table, c.rows, c.table_ld,
+             (const I*)idx, w, n, vecs, tx, c.scale, (T*)out, c.out_ld);
+  } else {
+    const unsigned gx = (unsigned)((n + ty - 1) / ty);
+    launch_k(lookup_bag_kernel<T, I, VEC>, dim3(gx, gy), LK_THREADS, 0, s, (const T*)table, c.rows, c.table_ld,
+             (const I*)idx, w, n, c.R, vecs, tx, c.scale, (T*)out, c.out_ld);
+  }
+}
+
+template <typename T, typename I>
+void go_lookup_v(const fwpkm_lookup_config& c, const void* table, const void* idx, const float* w, long long n,
+                 void* out, cudaStream_t s) {
+  if (rows_vec<T>(table, c.table_ld, c.width) && rows_vec<T>(out, c.out_ld, c.width))
+    go_lookup<T, I, 16 / (int)sizeof(T)>(c, table, idx, w, n, out, s);
+  else
+    go_lookup<T, I, 1>(c, table, idx, w, n, out, s);
+}
+
+template <typename I>
+int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const BackWork& w, int* sorted,
+            cudaStream_t s) {
+  const SortPlan sp = sort_plan(c.rows, P);
+  if (P <= RS_TILE) {
+    const size_t smem = 4 * (2 * (size_t)RS_TILE + sp.bins) + 2 * (size_t)RS_WARPS * sp.bins;
+    if (!raise_smem_limit((const void*)sort_small_kernel<I>, smem)) return -1;
+    launch_k(sort_small_kernel<I>, 1, RS_THREADS, smem, s, (const I*)idx, (int)P, c.rows, sp.bits, sp.passes,
+             w.key[0], w.pos[0]);
+    *sorted = 0;
+    return 1;
+  }
+  const size_t smem = 4 * 2 * (size_t)sp.bins + 2 * (size_t)RS_WARPS * sp.bins;
+  if (!raise_smem_limit((const void*)sort_scatter_kernel<I>, smem)) return -1;
+  const int own = sp.tiles <= RS_OWN_SCAN;
+  int nl = 0;
+  for (int pass = 0; pass < sp.passes; ++pass) {
+    const int from = (pass + 1) & 1, to = pass & 1;
+    Source<I> src{(const I*)idx, pass ? w.key[from] : nullptr, pass ? w.pos[from] : nullptr, c.rows};
+    launch_k(sort_hist_kernel<I>, sp.tiles, RS_THREADS, 0, s, src, P, pass * sp.per, sp.bins, w.hist);
+    ++nl;
+    if (!own) {
+      launch_k(sort_scan_kernel, (sp.bins + 127) / 128, 128, 0, s, w.hist, w.total, sp.tiles, sp.bins);
+      ++nl;
+    }
+    launch_k(sort_scatter_kernel<I>, sp.tiles, RS_THREADS, smem, s, src, P, pass * sp.per, sp.bins,
+             (const uint32_t*)w.hist, (const uint32_t*)w.total, sp.tiles, own, w.key[to], w.pos[to]);
+    ++nl;
+    *sorted = to;
+  }
+  return nl;
+}
+
+template <typename T, typename G, int VEC>
+int go_sum(const fwpkm_lookup_config& c, SegArgs a, const void* d_out, void* d_table, cudaStream_t s) {
+  a.vecs = c.width / VEC;
+  a.tx_n = row_threads(a.vecs);
+  const int ty = LK_THREADS / a.tx_n;
+  const unsigned gy = (unsigned)((a.vecs + a.tx_n - 1) / a.tx_n);
+  const unsigned sb = (unsigned)((a.ranges + ty - 1) / ty);
+  // dense gradient: CTAs that zero the rows nothing reads, up to four per SM, each at least
+  // 8 warps x 32 rows (column blocks share one row split: only blockIdx.y == 0 has them)
+  long long zb = 0;
+  if (!a.accumulate) {
+    zb = (a.rows + 255) / 256;
+    if (zb > 148 * 4) zb = 148 * 4;
+  }
+  if (sb + zb == 0) return 0;
+  int nl = 0;
+  if (gy == 1) {
+    launch_k(lookup_sum_kernel<T, G, VEC>, dim3(sb + (unsigned)zb), LK_THREADS, 0, s, a, (const T*)d_out,
+             (G*)d_table, (int)sb);
+    ++nl;
+  } else {
+    if (zb) {
+      launch_k(lookup_sum_kernel<T, G, VEC>, dim3((unsigned)zb), LK_THREADS, 0, s, a, (const T*)d_out, (G*)d_table, 0);
+      ++nl;
+    }
+    if (sb) {
+      launch_k(lookup_sum_kernel<T, G, VEC>, dim3(sb, gy), LK_THREADS, 0, s, a, (const T*)d_out, (G*)d_table,
+               (int)sb);
+      ++nl;
+    }
+  }
+  if (a.ranges > 1) {
+    launch_k(lookup_join_kernel<G, VEC>, dim3(sb, gy), LK_THREADS, 0, s, a, (G*)d_table);
+    ++nl;
+  }
+  return nl;
+}
+
+template <typename T, typename G>
+int go_sum_v(const fwpkm_lookup_config& c, const SegArgs& a, const void* d_out, void* d_table, cudaStream_t s) {
+  if (rows_vec<T>(d_out, c.out_ld, c.width) && rows_vec<G>(d_table, a.grad_ld, c.width))
+    return go_sum<T, G, 16 / (int)sizeof(T)>(c, a, d_out, d_table, s);
+  return go_sum<T, G, 1>(c, a, d_out, d_table, s);
+}
+
+template <typename T, typename I, int VEC>
+void go_dw(const fwpkm_lookup_config& c, const void* table, const void* idx, const void* d_out, long long n,
+           float* dw, cudaStream_t s) {
+  const long long jobs = n * ((c.R + DW_U - 1) / DW_U);
+  const unsigned g = (unsigned)((jobs + LK_THREADS / 32 - 1) / (LK_THREADS / 32));
+  launch_k(lookup_dw_kernel<T, I, VEC>, g, LK_THREADS, 0, s, (const T*)table, c.rows, c.table_ld, (const I*)idx,
+           (const T*)d_out, c.out_ld, n, c.R, c.width / VEC, c.scale, dw);
+}
+
+template <typename T, typename I>
+void go_dw_v(const fwpkm_lookup_config& c, const void* table, const void* idx, const void* d_out, long long n,
+             float* dw, cudaStream_t s) {
+  if (rows_vec<T>(table, c.table_ld, c.width) && rows_vec<T>(d_out, c.out_ld, c.width))
+    go_dw<T, I, 16 / (int)sizeof(T)>(c, table, idx, d_out, n, dw, s);
+  else
+    go_dw<T, I, 1>(c, table, idx, d_out, n, dw, s);
+}
+
+}  // namespace
+}  // namespace fwpkm
+
+using namespace fwpkm;
+
+extern "C" {
+
+fwpkm_status fwpkm_lookup(const fwpkm_lookup_config* cfg, const void* table, const void* idx, const float* w,
+                          long long n, void* out, void* stream) {
+  NvtxRange nvtx_range("fwpkm_lookup");
+  const fwpkm_status cs = check_lookup(cfg, n);
+  if (cs != FWPKM_OK) return cs;
+  if (n == 0) return FWPKM_OK;
+  const size_t es = dsize(cfg->dtype);
+  if (!table || !idx || !out || !ptr_al(table, es) || !ptr_al(out, es) || (w && !ptr_al(w, 4)) ||
+      !ptr_al(idx, cfg->idx_dtype == FWPKM_I64 ? 8 : 4))
+    return FWPKM_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  const bool i64 = cfg->idx_dtype == FWPKM_I64;
+  if (cfg->dtype == FWPKM_BF16) {
+    if (i64) go_lookup_v<__nv_bfloat16, long long>(*cfg, table, idx, w, n, out, s);
+    else go_lookup_v<__nv_bfloat16, int>(*cfg, table, idx, w, n, out, s);
+  } else {
+    if (i64) go_lookup_v<float, long long>(*cfg, table, idx, w, n, out, s);
+    else go_lookup_v<float, int>(*cfg, table, idx, w, n, out, s);
+  }
+  return done(1);
+}
+
+fwpkm_status fwpkm_lookup_backward_workspace_size(const fwpkm_lookup_config* cfg, long long n, size_t* bytes) {
+  const fwpkm_status cs = check_lookup(cfg, n);
+  if (cs != FWPKM_OK) return cs;
+  if (!bytes) return FWPKM_ERR_INVALID_ARG;
+  *bytes = back_carve(*cfg, n * cfg->R, nullptr, nullptr);
+  return FWPKM_OK;
+}
+
+fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* table, const void* idx, const float* w,
+                                   const void* d_out, long long n, void* d_table, long long grad_ld, int grad_dtype,
+                                   int accumulate, float* dw, void* workspace, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("fwpkm_lookup_backward");
+  const fwpkm_status cs = check_lookup(cfg, n);
+  if (cs != FWPKM_OK) return cs;
+  if (d_table && (grad_ld < cfg->width || (grad_dtype != FWPKM_F32 && grad_dtype != FWPKM_BF16)))
+    return FWPKM_ERR_INVALID_ARG;
+  const size_t es = dsize(cfg->dtype);
+  if (d_table && !ptr_al(d_table, dsize(grad_dtype))) return FWPKM_ERR_INVALID_ARG;
+  if (n > 0) {
+    if (!idx || !d_out || !ptr_al(d_out, es) || (w && !ptr_al(w, 4)) || (dw && (!table || !ptr_al(table, es) || !ptr_al(dw, 4))) ||
+        !ptr_al(idx, cfg->idx_dtype == FWPKM_I64 ? 8 : 4))
+      return FWPKM_ERR_INVALID_ARG;
+    if (d_table) {
+      if (!workspace || !ptr_al(workspace, 256)) return FWPKM_ERR_INVALID_ARG;
+      if (ws_bytes < back_carve(*cfg, n * cfg->R, nullptr, nullptr)) return FWPKM_ERR_WORKSPACE;
+    }
+  }
+  if (n == 0 && (!d_table || accumulate)) return FWPKM_OK;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaGetLastError();
+  PdlScope pdl(true);
+  const bool i64 = cfg->idx_dtype == FWPKM_I64, bf = cfg->dtype == FWPKM_BF16;
+  const long long P = n * cfg->R;
+  int nl = 0;
+  if (d_table) {
+    SegArgs a = {};
+    a.P = P;
+    a.rows = cfg->rows; a.out_ld = cfg->out_ld; a.grad_ld = grad_ld;
+    a.R = cfg->R; a.width = cfg->width; a.scale = cfg->scale; a.accumulate = accumulate != 0;
+    a.ranges = (P + SEG - 1) / SEG;
+    a.w = w;
+    if (P > 0) {
+      BackWork bw;
+      back_carve(*cfg, P, (char*)workspace, &bw);
+      int at = 0;
+      nl = i64 ? go_sort<long long>(*cfg, idx, P, bw, &at, s) : go_sort<int>(*cfg, idx, P, bw, &at, s);
+      if (nl < 0) return FWPKM_ERR_CUDA;
+      a.key = bw.key[at];
+      a.pos = bw.pos[at];
+      a.part = bw.part;
+    }
+    if (bf)
+      nl += grad_dtype == FWPKM_BF16 ? go_sum_v<__nv_bfloat16, __nv_bfloat16>(*cfg, a, d_out, d_table, s)
+                                     : go_sum_v<__nv_bfloat16, float>(*cfg, a, d_out, d_table, s);
+    else
+      nl += grad_dtype == FWPKM_BF16 ? go_sum_v<float, __nv_bfloat16>(*cfg, a, d_out, d_table, s)
+                                     : go_sum_v<float, float>(*cfg, a, d_out, d_table, s);
+  }
+  if (dw && n > 0) {
+    if (bf) {
+      if (i64) go_dw_v<__nv_bfloat16, long long>(*cfg, table, idx, d_out, n, dw, s);
+      else go_dw_v<__nv_bfloat16, int>(*cfg, table, idx, d_out, n, dw, s);
+    } else {
+      if (i64) go_dw_v<float, long long>(*cfg, table, idx, d_out, n, dw, s);
+      else go_dw_v<float, int>(*cfg, table, idx, d_out, n, dw, s);
+    }
+    ++nl;
+  }
+  return done(nl);
+}
+
+}  // extern "C"

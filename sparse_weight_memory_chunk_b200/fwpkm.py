@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_HERE, "libfwpkm.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_STATE, ERR_BAD_SLOT = \
     0, -1, -2, -3, -4, -5, -6, -7
 F32, BF16 = 0, 1
+I32, I64 = 0, 1
+BALANCE_KIND = {"load": 0, "entropy": 1}
 KEY_UPDATE, TARGET_NORM, LOOKAHEAD, GATE_WEIGHT = 1, 2, 4, 8
 DEFAULT_FLAGS = TARGET_NORM | LOOKAHEAD | GATE_WEIGHT
 KIND = {"gather": 1, "write": 2, "score": 3, "cartesian": 4, "sort": 5, "address": 6, "other": 7, "topk": 8,
@@ -59,6 +61,27 @@ class LayerParams(ctypes.Structure):
                 ("W_v", _P), ("gamma_v", _P), ("b_v", _P),
                 ("w_g", _P), ("gamma_g", _P), ("b_g", ctypes.c_float),
                 ("W_o", _P), ("gamma_o", _P), ("b_o", _P)]
+
+
+class LookupConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("table_ld", ctypes.c_longlong), ("out_ld", ctypes.c_longlong),
+                ("width", ctypes.c_int), ("R", ctypes.c_int), ("dtype", ctypes.c_int), ("idx_dtype", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class BalanceConfig(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_longlong), ("ld", ctypes.c_longlong), ("group_stride", ctypes.c_longlong),
+                ("groups", ctypes.c_int), ("experts", ctypes.c_int), ("k", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("kind", ctypes.c_int), ("coef", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("p", _P), ("sb", ctypes.c_longlong), ("sh", ctypes.c_longlong), ("st", ctypes.c_longlong)]
+
+
+class LinattnConfig(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int), ("d_v", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 def lib():
@@ -114,6 +137,21 @@ def lib():
             "fwpkm_addressing_metrics": ([_P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                           _P, ctypes.c_size_t, _P, _P, _P], ctypes.c_int),
         }
+        LC, BC, AC, HP = (ctypes.POINTER(t) for t in (LookupConfig, BalanceConfig, LinattnConfig, Heads))
+        ll, sz, i32 = ctypes.c_longlong, ctypes.c_size_t, ctypes.c_int
+        sig.update({
+            "fwpkm_lookup": ([LC, _P, _P, _P, ll, _P, _P], i32),
+            "fwpkm_lookup_backward_workspace_size": ([LC, ll, ctypes.POINTER(sz)], i32),
+            "fwpkm_lookup_backward": ([LC, _P, _P, _P, _P, ll, _P, ll, i32, i32, _P, _P, sz, _P], i32),
+            "fwpkm_balance_workspace_size": ([BC, ctypes.POINTER(sz)], i32),
+            "fwpkm_balance_loss": ([BC, _P, _P, _P, _P, sz, _P, _P, _P, _P, _P], i32),
+            "fwpkm_balance_loss_backward": ([BC, _P, _P, _P, _P, _P, _P], i32),
+            "fwpkm_linear_attention_workspace_size": ([AC, i32, i32, ctypes.POINTER(sz)], i32),
+            "fwpkm_linear_attention": ([AC, HP, HP, HP, i32, _P, _P, _P, HP, _P, _P, sz, _P], i32),
+            "fwpkm_linear_attention_backward": ([AC, HP, HP, HP, i32, _P, _P, _P, HP, _P, HP, HP, HP, _P, _P, sz, _P],
+                                                i32),
+            "fwpkm_linear_attention_step": ([AC, HP, HP, HP, i32, _P, _P, _P, HP, _P, _P], i32),
+        })
         for name, (args, res) in sig.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -238,6 +276,326 @@ def addressing_metrics(idx, N: int, window: int = 32768, workspace=None, stream=
     _check(lib().fwpkm_addressing_metrics(_ptr(idx), M, T, k, N, window, _ptr(workspace), workspace.numel(),
                                           _ptr(met), _ptr(cnt), _stream(stream)), "addressing_metrics")
     return met, cnt
+
+
+# ---- operators around the memory -------------------------------------------------------
+# Torch tensors in, torch tensors out; every call only enqueues on `stream` (default: the
+# current stream of the tensors' device).
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype(t, what):
+    import torch
+    if t.dtype == torch.float32:
+        return F32
+    _need(t.dtype == torch.bfloat16, f"{what} must be float32 or bfloat16, not {t.dtype}")
+    return BF16
+
+
+class _on:
+    """The stream handle of a call on `dev`, with `dev` current while the call is made."""
+
+    def __init__(self, dev, stream):
+        import torch
+        _need(dev.type == "cuda", "the tensors must be on a CUDA device")
+        self.cur = torch.cuda.current_device()
+        self.dev = self.cur if dev.index is None else dev.index
+        if stream is None:
+            stream = torch.cuda.current_stream(self.dev)
+        _need(stream.device_index == self.dev, "the stream is another device's than the tensors")
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.dev != self.cur:
+            import torch
+            torch.cuda.set_device(self.dev)
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.dev != self.cur:
+            import torch
+            torch.cuda.set_device(self.cur)
+
+
+def _side(t, dev, dtype, shape, what):
+    """A contiguous tensor of this type, shape and device (None passes)."""
+    if t is not None:
+        _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == dev and t.is_contiguous(),
+              f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace, nbytes, dev, what):
+    import torch
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _need(workspace.device == dev and workspace.is_contiguous(), f"{what}: the workspace must be contiguous, on {dev}")
+    return workspace
+
+
+def _scratch_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _lookup_config(table, idx, w, scale):
+    import torch
+    _need(table.dim() == 2 and (table.stride(1) == 1 or table.shape[1] <= 1),
+          "table must be [rows][width], its rows contiguous")
+    _need(idx.dtype in (torch.int32, torch.int64), "idx must be int32 or int64")
+    _need(idx.device == table.device and idx.is_contiguous(), "idx must be contiguous, on the table's device")
+    R = 1
+    if w is not None:
+        _need(idx.dim() >= 1, "with w the last axis of idx is the bag")
+        R = idx.shape[-1]
+        _side(w, table.device, torch.float32, idx.shape, "w")
+    lead = tuple(idx.shape[:-1]) if w is not None else tuple(idx.shape)
+    n = idx.numel() // R if R else 0
+    cfg = LookupConfig(table.shape[0], max(table.stride(0), table.shape[1]), table.shape[1], table.shape[1], R,
+                       _dtype(table, "table"), I64 if idx.dtype == torch.int64 else I32, scale)
+    return cfg, lead, n
+
+
+def lookup(table, idx, w=None, scale=1.0, out=None, stream=None):
+    """fwpkm_lookup: scale * table[idx], shape idx.shape + [width]; with weights w (fp32, the
+    shape of idx) the last axis of idx is summed: scale * sum_r w[.., r] table[idx[.., r]].
+    Indices outside the table read zeros."""
+    import torch
+    cfg, lead, n = _lookup_config(table, idx, w, scale)
+    shape = lead + (table.shape[1],)
+    if out is None:
+        out = torch.empty(shape, dtype=table.dtype, device=table.device)
+    _side(out, table.device, table.dtype, shape, "out")
+    with _on(table.device, stream) as s:
+        _check(lib().fwpkm_lookup(ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
+                                  None if w is None else w.data_ptr(), n, out.data_ptr(), s), "lookup")
+    return out
+
+
+def lookup_backward_workspace_size(table, idx, w=None) -> int:
+    cfg, _, n = _lookup_config(table, idx, w, 1.0)
+    out = ctypes.c_size_t(0)
+    _check(lib().fwpkm_lookup_backward_workspace_size(ctypes.byref(cfg), n, ctypes.byref(out)),
+           "lookup_backward_workspace_size")
+    return out.value
+
+
+def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumulate=False, grad_dtype=None, dw=None,
+                    need_dw=True, workspace=None, stream=None):
+    """fwpkm_lookup_backward: (d_table, dw) of lookup(table, idx, w, scale) from d_out.
+    d_table [rows][width] (grad_dtype, default the table's type) is written whole, or with
+    accumulate added to the rows that were read (then it must be given); dw (fp32, the shape
+    of idx) is None without w or with need_dw=False."""
+    import torch
+    cfg, lead, n = _lookup_config(table, idx, w, scale)
+    dev = table.device
+    _side(d_out, dev, table.dtype, lead + (table.shape[1],), "d_out")
+    _need(not accumulate or d_table is not None, "accumulate needs the d_table to add to")
+    if d_table is None:
+        d_table = torch.empty(table.shape, dtype=grad_dtype or table.dtype, device=dev)
+    _need(d_table.shape == table.shape and d_table.device == dev and (d_table.stride(1) == 1 or table.shape[1] <= 1)
+          and (table.shape[0] <= 1 or d_table.stride(0) >= table.shape[1]),
+          "d_table must have the table's shape and device, its rows contiguous and apart")
+    _need(grad_dtype is None or d_table.dtype == grad_dtype, "d_table is not of grad_dtype")
+    if w is None or not need_dw:
+        _need(dw is None, "dw needs w and need_dw")
+    else:
+        if dw is None:
+            dw = torch.empty(idx.shape, dtype=torch.float32, device=dev)
+        _side(dw, dev, torch.float32, idx.shape, "dw")
+    nb = ctypes.c_size_t(0)
+    _check(lib().fwpkm_lookup_backward_workspace_size(ctypes.byref(cfg), n, ctypes.byref(nb)), "lookup_backward")
+    ws = _scratch(workspace, nb.value, dev, "lookup_backward")
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_lookup_backward(ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
+                                           None if w is None else w.data_ptr(), d_out.data_ptr(), n,
+                                           d_table.data_ptr(), max(d_table.stride(0), table.shape[1]),
+                                           _dtype(d_table, "d_table"), int(accumulate),
+                                           None if dw is None else dw.data_ptr(), *_scratch_args(ws), s),
+               "lookup_backward")
+    return d_table, dw
+
+
+class BalanceLoss:
+    """What balance_loss returns: loss [G], counts [G][E] (None without idx), usage [G][E], and
+    the slope [G][E] that balance_loss_backward needs."""
+    __slots__ = ("loss", "counts", "usage", "slope", "kind", "coef")
+
+
+def _balance_config(x, idx, mask, kind, coef):
+    import torch
+    _need(x.dim() == 3 and (x.stride(2) == 1 or x.shape[2] <= 1), "x must be [groups][tokens][experts], its rows contiguous")
+    _need(kind in BALANCE_KIND, f"kind must be one of {sorted(BALANCE_KIND)}")
+    G, T, E = x.shape
+    k = 0
+    if idx is not None:
+        _need(idx.dim() == 3, "idx must be [groups][tokens][k]")
+        k = idx.shape[2]
+        _side(idx, x.device, torch.int32, (G, T, k), "idx")
+    if mask is not None:
+        _need(mask.dtype in (torch.bool, torch.uint8), "mask must be bool or uint8")
+        _side(mask, x.device, mask.dtype, (G, T), "mask")
+    return BalanceConfig(T, max(x.stride(1), E), x.stride(0) if G > 1 else 0, G, E, k, _dtype(x, "x"),
+                         BALANCE_KIND[kind], coef)
+
+
+def balance_loss(x, idx=None, mask=None, kind="load", coef=1.0, workspace=None, stream=None) -> BalanceLoss:
+    """fwpkm_balance_loss of router logits x [groups][tokens][experts] with the selections idx
+    [groups][tokens][k] int32 (kind "load"; optional for "entropy") and a mask
+    [groups][tokens] of the tokens that count."""
+    import torch
+    cfg = _balance_config(x, idx, mask, kind, coef)
+    dev, G, E = x.device, cfg.groups, cfg.experts
+    nb = ctypes.c_size_t(0)
+    _check(lib().fwpkm_balance_workspace_size(ctypes.byref(cfg), ctypes.byref(nb)), "balance_loss")
+    ws = _scratch(workspace, nb.value, dev, "balance_loss")
+    r = BalanceLoss()
+    r.kind, r.coef = kind, coef
+    f = torch.empty(2 * G * E + G, dtype=torch.float32, device=dev)
+    r.usage, r.slope, r.loss = f[:G * E].view(G, E), f[G * E:2 * G * E].view(G, E), f[2 * G * E:]
+    r.counts = None if idx is None else torch.empty(G, E, dtype=torch.int32, device=dev)
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_balance_loss(ctypes.byref(cfg), x.data_ptr(), None if idx is None else idx.data_ptr(),
+                                        None if mask is None else mask.data_ptr(), *_scratch_args(ws),
+                                        r.loss.data_ptr(), None if idx is None else r.counts.data_ptr(),
+                                        r.usage.data_ptr(), r.slope.data_ptr(), s), "balance_loss")
+    return r
+
+
+def balance_loss_backward(x, result: BalanceLoss, mask=None, d_loss=None, dx=None, stream=None):
+    """fwpkm_balance_loss_backward: dx [groups][tokens][experts] of balance_loss's result for
+    the same x and mask, from d_loss [groups] (None: ones)."""
+    import torch
+    cfg = _balance_config(x, None, mask, result.kind, result.coef)
+    dev, G, T, E = x.device, *x.shape
+    _side(result.slope, dev, torch.float32, (G, E), "result.slope")
+    _side(d_loss, dev, torch.float32, (G,), "d_loss")
+    if dx is None:
+        dx = torch.empty(G, T, E, dtype=x.dtype, device=dev)
+    _side(dx, dev, x.dtype, (G, T, E), "dx")
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_balance_loss_backward(ctypes.byref(cfg), x.data_ptr(),
+                                                 None if mask is None else mask.data_ptr(),
+                                                 result.slope.data_ptr(),
+                                                 None if d_loss is None else d_loss.data_ptr(), dx.data_ptr(), s),
+               "balance_loss_backward")
+    return dx
+
+
+def _heads(t, dev, dtype, B, H, T, w, what):
+    """A [B][H][T][w] tensor of any strides with contiguous rows."""
+    _need(t.dim() == 4 and tuple(t.shape) == (B, H, T, w) and t.dtype == dtype and t.device == dev,
+          f"{what} must be a {dtype} tensor of shape {(B, H, T, w)} on {dev}")
+    sb, sh, st, se = t.stride()
+    _need(se == 1 or w == 1, f"{what}: the rows must be contiguous")
+    return Heads(t.data_ptr(), sb, sh, st)
+
+
+def _linattn_args(q, k, v, log_decay, scale, lens):
+    import torch
+    _need(q.dim() == 4 and v.dim() == 4, "q, k, v must be [B][H][T][width]")
+    B, H, T, d = q.shape
+    dv, dev, dt = v.shape[3], q.device, q.dtype
+    hq = _heads(q, dev, dt, B, H, T, d, "q")
+    hk = _heads(k, dev, dt, B, H, T, d, "k")
+    hv = _heads(v, dev, dt, B, H, T, dv, "v")
+    ld = _side(log_decay, dev, torch.float32, (H,), "log_decay")
+    _need(ld is not None, "log_decay is needed")
+    ln = _side(lens, dev, torch.int32, (B,), "lens")
+    return LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale), hq, hk, hv, ld, ln, T
+
+
+def _rows_like(t, B, H, T, w):
+    """A new [B][H][T][w] tensor in the memory order [B][T][H][w] of a projection's output."""
+    import torch
+    return torch.empty(B, T, H, w, dtype=t.dtype, device=t.device).transpose(1, 2)
+
+
+def linear_attention_workspace_size(q, v, backward=False) -> int:
+    cfg = LinattnConfig(q.shape[0], q.shape[1], q.shape[3], v.shape[3], _dtype(q, "q"), 1.0)
+    out = ctypes.c_size_t(0)
+    _check(lib().fwpkm_linear_attention_workspace_size(ctypes.byref(cfg), q.shape[2], int(backward),
+                                                       ctypes.byref(out)), "linear_attention_workspace_size")
+    return out.value
+
+
+def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, sT=None, final_state=False,
+                     workspace=None, stream=None):
+    """fwpkm_linear_attention: (o, sT) of q, k [B][H][T][d], v [B][H][T][d_v] (any strides with
+    contiguous rows), log_decay [H] fp32, start states s0 [B][H][d][d_v] fp32 and lengths lens
+    [B] int32.  sT is None unless given or asked for with final_state.  Rows of o behind a
+    sequence's end are left as they were (a new o holds anything there)."""
+    import torch
+    cfg, hq, hk, hv, ld, ln, T = _linattn_args(q, k, v, log_decay, scale, lens)
+    dev, B, H, d, dv = q.device, cfg.B, cfg.H, cfg.d, cfg.d_v
+    if o is None:
+        o = _rows_like(v, B, H, T, dv)
+    ho = _heads(o, dev, q.dtype, B, H, T, dv, "o")
+    if sT is None and final_state:
+        sT = torch.empty(B, H, d, dv, dtype=torch.float32, device=dev)
+    p0 = _side(s0, dev, torch.float32, (B, H, d, dv), "s0")
+    pT = _side(sT, dev, torch.float32, (B, H, d, dv), "sT")
+    nb = ctypes.c_size_t(0)
+    _check(lib().fwpkm_linear_attention_workspace_size(ctypes.byref(cfg), T, 0, ctypes.byref(nb)), "linear_attention")
+    ws = _scratch(workspace, nb.value, dev, "linear_attention")
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_linear_attention(ctypes.byref(cfg), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), T,
+                                            ld, ln, p0, ctypes.byref(ho), pT, *_scratch_args(ws), s),
+               "linear_attention")
+    return o, sT
+
+
+def linear_attention_backward(q, k, v, log_decay, d_o, scale=1.0, s0=None, d_sT=None, lens=None, grads=None, ds0=None,
+                              state_grad=True, workspace=None, stream=None):
+    """fwpkm_linear_attention_backward: (dq, dk, dv, ds0) of linear_attention from d_o and the
+    final state's gradient d_sT (None: zero).  `grads`: (dq, dk, dv) to fill; ds0 is None with
+    state_grad=False.  Rows behind a sequence's end are left as they were."""
+    import torch
+    cfg, hq, hk, hv, ld, ln, T = _linattn_args(q, k, v, log_decay, scale, lens)
+    dev, dt, B, H, d, dv = q.device, q.dtype, cfg.B, cfg.H, cfg.d, cfg.d_v
+    ho = _heads(d_o, dev, dt, B, H, T, dv, "d_o")
+    if grads is None:
+        grads = (_rows_like(q, B, H, T, d), _rows_like(q, B, H, T, d), _rows_like(v, B, H, T, dv))
+    hg = [_heads(t, dev, dt, B, H, T, w, n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
+    if ds0 is None and state_grad:
+        ds0 = torch.empty(B, H, d, dv, dtype=torch.float32, device=dev)
+    p0 = _side(s0, dev, torch.float32, (B, H, d, dv), "s0")
+    pT = _side(d_sT, dev, torch.float32, (B, H, d, dv), "d_sT")
+    pd = _side(ds0, dev, torch.float32, (B, H, d, dv), "ds0")
+    nb = ctypes.c_size_t(0)
+    _check(lib().fwpkm_linear_attention_workspace_size(ctypes.byref(cfg), T, 1, ctypes.byref(nb)),
+           "linear_attention_backward")
+    ws = _scratch(workspace, nb.value, dev, "linear_attention_backward")
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_linear_attention_backward(ctypes.byref(cfg), ctypes.byref(hq), ctypes.byref(hk),
+                                                     ctypes.byref(hv), T, ld, ln, p0, ctypes.byref(ho), pT,
+                                                     ctypes.byref(hg[0]), ctypes.byref(hg[1]), ctypes.byref(hg[2]), pd,
+                                                     *_scratch_args(ws), s), "linear_attention_backward")
+    return (*grads, ds0)
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=None, state_out=None, in_place=True,
+                          stream=None):
+    """fwpkm_linear_attention_step: (o, new state) of a few new tokens [B][H][n][..] from the
+    states [B][H][d][d_v], which are updated in place unless state_out is given or
+    in_place=False (then a new tensor is)."""
+    import torch
+    cfg, hq, hk, hv, ld, ln, T = _linattn_args(q, k, v, log_decay, scale, lens)
+    dev, B, H, d, dv = q.device, cfg.B, cfg.H, cfg.d, cfg.d_v
+    if o is None:
+        o = _rows_like(v, B, H, T, dv)
+    ho = _heads(o, dev, q.dtype, B, H, T, dv, "o")
+    if state_out is None:
+        state_out = state if in_place else torch.empty_like(state)
+    ps = _side(state, dev, torch.float32, (B, H, d, dv), "state")
+    po = _side(state_out, dev, torch.float32, (B, H, d, dv), "state_out")
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_linear_attention_step(ctypes.byref(cfg), ctypes.byref(hq), ctypes.byref(hk),
+                                                 ctypes.byref(hv), T, ld, ln, ps, ctypes.byref(ho), po, s),
+               "linear_attention_step")
+    return o, state_out
 
 
 class State:
