@@ -550,14 +550,19 @@ fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const 
                                          const int32_t* lens, const float* state, const fwpkm_heads* o,
                                          float* state_out, void* stream);
 
+/* Wait for `stream` and return the device status that linear-attention kernels on the current
+ * device have latched since the last call (FWPKM_ERR_TIMEOUT: a bounded wait ran out and that
+ * call's results are not valid), clearing it. */
+fwpkm_status fwpkm_linear_attention_sync(void* stream);
+
 /* Wait for `stream` and return the latched device status (FWPKM_OK,
  * FWPKM_ERR_TIMEOUT, FWPKM_ERR_BAD_SLOT), clearing it (device word and host copy). */
 fwpkm_status fwpkm_sync(fwpkm_state* st, void* stream);
 
 /* Test hook of the timeout path (no counterpart in the paper).  Each of the next
  * `n_launches` launches made by this process of a kernel with a bounded wait (the
- * tensor-core scoring, key step and projections; the one-launch addressing step; the
- * persistent value loop of fwpkm_run_sequence with frozen keys) first waits on
+ * tensor-core scoring, key step and projections; linear attention on the tensor cores (per
+ * pass); the one-launch addressing step; the persistent value loop of fwpkm_run_sequence with frozen keys) first waits on
  * something that nothing completes: an mbarrier for the MMA-issuing thread, or an
  * arrival count that no launch reaches for the value loop.  That wait is bounded like
  * every other wait in those kernels (0.2 s): it runs out, the kernel takes its abort

@@ -83,7 +83,7 @@ scan_kernel(ScanArgs a, int lj, int tb, int local) {
                             : (a.s_in ? a.s_in + (size_t)bh * cells : nullptr);
     if (src) {
       const long long si = slot ? a.dv : a.si, sj = slot ? 1 : a.sj;
-      const float f = slot ? 1.f : a.in_scale;
+      const float f = slot || n == 0 ? 1.f : a.in_scale;
       const bool vec = sj == 1 && (a.dv & 3) == 0 && (((uintptr_t)src) & 15) == 0;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -218,7 +218,7 @@ scan_kernel(ScanArgs a, int lj, int tb, int local) {
                      : (a.s_out && g == a.nseg - 1 ? a.s_out + (size_t)bh * cells : nullptr);
   if (!dst) return;
   const long long si = local ? a.dv : a.si, sj = local ? 1 : a.sj;
-  const float w = local ? 1.f : a.st_scale * (a.out_decay && n > 0 ? a1 : 1.f);
+  const float w = local || n == 0 ? 1.f : a.st_scale * (a.out_decay ? a1 : 1.f);
   const bool vec = sj == 1 && (a.dv & 3) == 0 && (((uintptr_t)dst) & 15) == 0;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -250,7 +250,7 @@ scan_combine_kernel(ScanArgs a) {
   const float ld = a.log_decay[h];
   const int i = (int)(x / a.dv), j = (int)(x - (size_t)i * a.dv);
   float* slot = a.slots + (size_t)bh * a.nseg * cells + x;
-  float E = a.s_in ? a.s_in[(size_t)bh * cells + i * a.si + j * a.sj] * a.in_scale : 0.f;
+  float E = a.s_in ? a.s_in[(size_t)bh * cells + i * a.si + j * a.sj] * (n == 0 ? 1.f : a.in_scale) : 0.f;
   slot[(size_t)(a.nseg - 1) * cells] = E;
   for (int g0 = 0; g0 < a.nseg - 1; g0 += 8) {
     float loc[8];
@@ -374,8 +374,10 @@ ScanArgs forward_args(const fwpkm_linattn_config& c, int T, const float* log_dec
   return a;
 }
 
-int segments_of(const ScanArgs& a, int dtype) {
-  return scan_tc_takes(a, dtype) ? scan_tc_segments(a) : scan_segments(a);
+// Segments a pass of this shape may use, whatever its pointers and strides.
+int most_segments(const ScanArgs& a, int dtype) {
+  const int cc = scan_segments(a), tc = scan_tc_shape(a, dtype) ? scan_tc_segments(a) : 1;
+  return cc > tc ? cc : tc;
 }
 size_t slot_bytes(const ScanArgs& a, int nseg) {
   return nseg > 1 ? ((size_t)a.B * a.H * nseg * a.d * a.dv * 4 + 255) / 256 * 256 : 0;
@@ -437,14 +439,12 @@ fwpkm_status fwpkm_linear_attention_workspace_size(const fwpkm_linattn_config* c
     ScanArgs p[3];
     grad_args(*cfg, T, nullptr, nullptr, p);
     for (int i = 0; i < 3; ++i) {
-      const int cc = segments_of(p[i], cfg->dtype), gen = scan_segments(p[i]);
-      const size_t b = slot_bytes(p[i], cc > gen ? cc : gen);
+      const size_t b = slot_bytes(p[i], most_segments(p[i], cfg->dtype));
       if (b > most) most = b;
     }
   } else {
     const ScanArgs a = forward_args(*cfg, T, nullptr, nullptr);
-    const int cc = segments_of(a, cfg->dtype), gen = scan_segments(a);
-    most = slot_bytes(a, cc > gen ? cc : gen);
+    most = slot_bytes(a, most_segments(a, cfg->dtype));
   }
   *bytes = most;
   return FWPKM_OK;
@@ -546,6 +546,12 @@ fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const 
   cudaGetLastError();
   PdlScope pdl(true);
   return la_done(launch_scan(a, cfg->dtype, 1, (cudaStream_t)stream));
+}
+
+fwpkm_status fwpkm_linear_attention_sync(void* stream) {
+  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return la_done(-1);
+  const int st = take_scan_status();
+  return st < 0 ? la_done(-1) : status_of_device(st);
 }
 
 }  // extern "C"

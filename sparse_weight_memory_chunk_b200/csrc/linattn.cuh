@@ -40,11 +40,14 @@ __device__ __forceinline__ int scan_len(const ScanArgs& a, int b) {
   return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 
-// Tensor-core pass (linattn_tc.cu): whether it takes this pass, and the launch (the number
-// of kernels, or < 0 on a CUDA error).
+// Tensor-core pass (linattn_tc.cu): whether it takes passes of this shape, and this pass (its
+// pointers and strides too); the launch (the number of kernels, or < 0 on a CUDA error); the
+// status its kernels latched since the last call (a DEV_* value, cleared; < 0: CUDA error).
+bool scan_tc_shape(const ScanArgs& a, int dtype);
 bool scan_tc_takes(const ScanArgs& a, int dtype);
 int scan_tc_segments(const ScanArgs& a);
 int launch_scan_tc(const ScanArgs& a, cudaStream_t s);
+int take_scan_status();
 int launch_scan_combine(const ScanArgs& a, cudaStream_t s);
 
 }  // namespace fwpkm

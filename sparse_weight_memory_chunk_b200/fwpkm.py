@@ -150,6 +150,7 @@ def lib():
             "fwpkm_linear_attention": ([AC, HP, HP, HP, i32, _P, _P, _P, HP, _P, _P, sz, _P], i32),
             "fwpkm_linear_attention_backward": ([AC, HP, HP, HP, i32, _P, _P, _P, HP, _P, HP, HP, HP, _P, _P, sz, _P],
                                                 i32),
+            "fwpkm_linear_attention_sync": ([_P], i32),
             "fwpkm_linear_attention_step": ([AC, HP, HP, HP, i32, _P, _P, _P, HP, _P, _P], i32),
         })
         for name, (args, res) in sig.items():
@@ -596,6 +597,15 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
                                                  ctypes.byref(hv), T, ld, ln, ps, ctypes.byref(ho), po, s),
                "linear_attention_step")
     return o, state_out
+
+
+def linear_attention_sync(device=None, stream=None):
+    """fwpkm_linear_attention_sync: wait for the stream and raise what linear-attention kernels
+    on the device have latched (a wait that timed out)."""
+    import torch
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    with _on(dev, stream) as s:
+        _check(lib().fwpkm_linear_attention_sync(s), "linear_attention_sync")
 
 
 class State:
