@@ -9,25 +9,29 @@
 //   E' = a^m E + U
 // The descending pass is the same with the rows of the tile mirrored: its tiles end at the
 // chunk's first token, so every formula takes u = 127 - row.
+// a^(t-s) = R_t B_s with B_s = a^(127-s), R_t = a^(t-127), so P is weighted by column, E enters
+// as a^128 E, and R_t multiplies the finished row of O.  A head whose a^128 is out of range
+// (|log a^128| > LA_RANGE) takes the weights element by element and scales Q E in place.
 //
 // Precision: the inputs are bf16, exact operands.  What is not exact in bf16 enters as pieces:
-// P (weighted) and E as hi + lo (2^-18 left out; O is rounded to bf16 afterwards), the
-// weighted keys of U as hi + mid + lo (exact to fp32, so the fp32 state that is handed on
-// agrees with fp32 arithmetic).  E is kept in fp32 registers and U is a fresh accumulator per
-// chunk, so the tensor cores' running sums span one chunk only.
+// P (weighted) and E as hi + lo (2^-17 left out; O is rounded to bf16 afterwards), the
+// weighted keys of U as hi + mid + lo where the state is handed on in fp32 (exact to fp32),
+// else as two.  U adds the small pieces first, so few of the accumulator's roundings (which
+// truncate) are at full size: the state is 9e-8 off against 6e-7 the other way round.  E is
+// kept in fp32 registers and U is a fresh accumulator per chunk, so the tensor cores' running
+// sums span one chunk only.
 //
-// CTA = one head (and segment): warp 0 issues TMA loads (K, V two stages, Q one), warp 1 owns
-// TMEM and issues the MMAs (one thread), warps 2-9 do the elementwise work: warp w reads
-// TMEM lanes 32 (w % 4).. and column half (w - 2) / 4.  TMEM (512 columns): P fp32, overwritten
-// in place by its two bf16 pieces (operand A of P V); O; U; two pieces of the weighted,
-// transposed keys (operand A of U; the high piece waits in registers and takes the low one's
-// place: U's large terms come last, so few of the accumulator's roundings are at full size,
-// 2e-7 of the state instead of 6e-7 the other way round).  Per chunk, in order:
-//   MMA    P(c)   Q E(c)          U lo, mid           U hi, P V              P(c+1) ..
-//   math       K pieces(c) ......  P pieces, O scale ...  E update, E pieces, O out
-// Bound: HBM for d = d_v = 128 (1 KB per token and head against 8 tensor products of
-// 128 x 128 per token: 0.5 us of MMA and ~0.5 us of elementwise work per 0.7 us of HBM time
-// per chunk and SM at the measured rates).
+// CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one;
+// the rows of O leave through V's stage), warp 1 owns TMEM and issues the MMAs (one thread),
+// warps 4-19 do the elementwise work: warp w reads TMEM lanes 32 (w % 4).. and column group
+// (w - 4) / 4.  TMEM (512 columns): P fp32, overwritten in place by its two bf16 pieces
+// (operand A of P V); O; U; two pieces of the weighted, transposed keys (operand A of U; the
+// high piece waits in registers and takes the low one's place).  Per chunk c, in order:
+//   MMA    U lo, mid(c)    P(c)        U hi(c)     Q E(c)               P V(c)
+//   math   E pieces(c-1), O out(c-1)   K hi        P pieces(c)    E(c)  K pieces(c+1)
+// so the MMAs of a chunk (8 products of 128^3, 4096 cycles at the dense rate) follow one another
+// while the elementwise work is done beside them.
+// Bound: HBM for d = d_v = 128 (128 KB per chunk, 5500 cycles of an SM's share at 6.46 TB/s).
 #include <cstdio>
 
 #include "linattn.cuh"
@@ -40,9 +44,16 @@ using namespace sm100;
 namespace {
 
 constexpr int LC = 128;                  // tokens per chunk
-constexpr int LA_MATH_WARPS = 8;
-constexpr int LA_THREADS = (2 + LA_MATH_WARPS) * 32;
+// Four warps of roles (two idle: register shares go by warpgroups) and sixteen of elementwise
+// work, four per scheduler: with eight the kernel waited on latency (0.24 instructions per
+// cycle and scheduler).  640 threads launch at 96 registers; the roles give theirs up for the
+// others: 128 x 64 + 512 x 104 = 61440 = 640 x 96.
+constexpr int LA_ROLE_WARPS = 4, LA_MATH_WARPS = 16;
+constexpr int LA_THREADS = (LA_ROLE_WARPS + LA_MATH_WARPS) * 32;
+constexpr int LA_ROLE_REGS = 64, LA_MATH_REGS = 104;
+static_assert(LA_ROLE_WARPS * 32 * LA_ROLE_REGS + LA_MATH_WARPS * 32 * LA_MATH_REGS <= LA_THREADS * 96, "registers");
 constexpr uint64_t LA_TIMEOUT_NS = 200ull * 1000 * 1000;  // any single wait
+constexpr float LA_RANGE = 60.f;         // largest |log a^128| taken through column weights
 constexpr int LA_BLOCK = LC * 128;       // bytes of a 64-column block of 128 rows
 
 __device__ int g_la_status = DEV_OK;     // latched by a kernel whose wait ran out
@@ -51,14 +62,15 @@ __device__ int g_la_status = DEV_OK;     // latched by a kernel whose wait ran o
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_K1 = 448, TM_COLS = 512;
 
 struct TcBars {
-  uint64_t full_q, full_kv[2], p, o1, kt, u1, mid, u2, o2[2], next, drain, stall;
+  uint64_t full_q, full_k[2], full_v[2], free_k[2], staged[2], o2[2];
+  uint64_t p, o1, kt, khi, u1, mid, u2, next, drain, stall;
 };
 
 template <int DK, int DV>
 struct TcSmem {
   static constexpr int Q = LC * DK * 2, K = LC * DK * 2, V = LC * DV * 2, E = DK * DV * 2;
   static constexpr int off_k = Q, off_v = off_k + 2 * K, off_e = off_v + 2 * V, off_tab = off_e + 2 * E;
-  static constexpr int need = off_tab + 4 * (LC + 4) + (int)sizeof(TcBars) + 16 + 1024;
+  static constexpr int need = off_tab + 4 * (2 * LC + 4) + (int)sizeof(TcBars) + 16 + 1024;
   // one CTA per SM: each holds all of TMEM
   static constexpr int bytes = need > 120 * 1024 ? need : 120 * 1024;
 };
@@ -80,11 +92,9 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, volatile
   }
   return true;
 }
-// The same for a whole warp: one lane waits, all learn the verdict (and stay converged).
-__device__ __forceinline__ bool la_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
-  int ok = lane == 0 ? (la_wait(bar, parity, abort) ? 1 : 0) : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  return ok != 0;
+// The same for a whole warp, converged afterwards: true only if every lane saw the phase.
+__device__ __forceinline__ bool la_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, la_wait(bar, parity, abort)) != 0;
 }
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -92,13 +102,18 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (globaltimer() - t0 > LA_TIMEOUT_NS) return;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // rounded to nearest
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float low_f(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float high_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// The upper halves of two floats (bf16, truncated) as a pair, and what truncation leaves.
+__device__ __forceinline__ uint32_t pack_high(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ void below_high(float& x, float& y) {
+  sub2(x, y, __uint_as_float(__float_as_uint(x) & 0xffff0000u), __uint_as_float(__float_as_uint(y) & 0xffff0000u));
+}
 
 // Byte of element (row, col) in a tile of 64-column blocks of `rows` 128-byte rows, swizzled.
 __device__ __forceinline__ uint32_t sw_off(int row, int col, int rows) {
@@ -110,19 +125,20 @@ struct TcCoord {
 };
 struct TcPass {
   ScanArgs a;
-  TcCoord cq, ck, cv;
+  TcCoord cq, ck, cv, co;
   int local, stall;
 };
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(LA_THREADS, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv, const TcPass ps) {
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const TcPass ps) {
   using SM = TcSmem<DK, DV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = smem, *sk = smem + SM::off_k, *sv = smem + SM::off_v, *se = smem + SM::off_e;
-  float* pw = (float*)(smem + SM::off_tab);  // [LC + 1] a^j
+  float* bw = (float*)(smem + SM::off_tab);  // [LC] column weights B_s
+  float* pw = bw + LC;                       // [LC + 1] a^j
   TcBars* bar = (TcBars*)(pw + LC + 4);
   uint32_t* tmem_slot = (uint32_t*)(bar + 1);
   volatile int* abort = (volatile int*)(tmem_slot + 1);
@@ -130,18 +146,23 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   const ScanArgs& a = ps.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool local = ps.local != 0;
+  const bool three = a.s_out != nullptr;  // the state leaves in fp32
   const int bh = blockIdx.x, g = blockIdx.y;
   const int b = bh / a.H, h = bh - b * a.H;
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->full_q, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar->full_kv[i], 1);
+      mbar_init(&bar->full_k[i], 1);
+      mbar_init(&bar->full_v[i], 1);
+      mbar_init(&bar->free_k[i], 1);
+      mbar_init(&bar->staged[i], LA_MATH_WARPS);
       mbar_init(&bar->o2[i], 1);
     }
     mbar_init(&bar->p, 1);
     mbar_init(&bar->o1, 1);
     mbar_init(&bar->kt, LA_MATH_WARPS);
+    mbar_init(&bar->khi, LA_MATH_WARPS);
     mbar_init(&bar->u1, 1);
     mbar_init(&bar->mid, LA_MATH_WARPS);
     mbar_init(&bar->u2, 1);
@@ -166,6 +187,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   const int t0 = min(n, g * a.seg_len), t1 = min(n, t0 + a.seg_len);  // positions along the pass
   const int chunks = (t1 - t0 + LC - 1) / LC;
   const float ld = a.log_decay[h];
+  const bool fast = fabsf(ld) * (float)LC <= LA_RANGE;
   const float* init = nullptr;
   long long isi = a.dv, isj = 1;
   float in_scale = 1.f;
@@ -180,35 +202,61 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       in_scale = n == 0 ? 1.f : a.in_scale;
     }
   }
-  // first token row of the tile of chunk c: ascending, or ending at the chunk's first token
+  // first token row of the tile of chunk c (ascending, or ending at the chunk's first token),
+  // and the chunk's tokens
   auto tile_t = [&](int c) { return a.reverse ? n - (t0 + c * LC) - LC : t0 + c * LC; };
+  auto tokens = [&](int c) { return min(LC, t1 - t0 - c * LC); };
 
-  int kv_loads = 0, q_loads = 0;  // producer: chunks whose loads were issued
+  int k_loads = 0, v_loads = 0, q_loads = 0;  // producer: chunks whose loads were issued
+  if (warp < LA_ROLE_WARPS) regs_dec<LA_ROLE_REGS>();
   if (warp == 0) {
     if (lane == 0) {
-      // ---------------- TMA producer ----------------
+      // ---------------- TMA: loads of K, V, Q; stores of O ----------------
       auto load = [&](const CUtensorMap* m, uint8_t* dst, int width, uint64_t* fb, const TcCoord& cc, int c) {
+        mbar_expect_tx(fb, (uint32_t)(LC * width * 2));
         for (int x = 0; x < width; x += 64)
           tma_load_4d(dst + (x >> 6) * LA_BLOCK, m, fb, x, tile_t(c), h * cc.h, b * cc.b);
       };
-      bool ok = true;
-      for (int c = 0; c <= chunks && ok; ++c) {
-        const int cq = c - 1;  // Q of the chunk before, once Q of the one before that was read
-        if (!local && cq >= 0) {
-          if (cq >= 1 && !(ok = la_wait(&bar->o1, (cq - 1) & 1, abort))) break;
-          mbar_expect_tx(&bar->full_q, SM::Q);
-          load(&mq, sq, DK, &bar->full_q, ps.cq, cq);
-          ++q_loads;
+      auto load_k = [&](int c) {
+        if (c >= chunks) return;
+        load(&mk, sk + (c & 1) * SM::K, DK, &bar->full_k[c & 1], ps.ck, c);
+        ++k_loads;
+      };
+      auto load_v = [&](int c) {
+        if (c >= chunks) return;
+        load(&mv, sv + (c & 1) * SM::V, DV, &bar->full_v[c & 1], ps.cv, c);
+        ++v_loads;
+      };
+      auto load_q = [&](int c) {
+        if (local || c >= chunks) return;
+        load(&mq, sq, DK, &bar->full_q, ps.cq, c);
+        ++q_loads;
+      };
+      load_k(0);
+      load_v(0);
+      load_q(0);
+      load_k(1);
+      load_v(1);
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t ph = (c >> 1) & 1;
+        if (!la_wait(&bar->free_k[c & 1], ph, abort)) break;
+        load_k(c + 2);
+        if (local) {
+          load_v(c + 2);
+          continue;
         }
-        if (c < chunks) {
-          // K, V of chunk c once the products of chunk c - 2 have read their stage
-          if (c >= 2 && !(ok = la_wait(&bar->o2[c & 1], ((c - 2) >> 1) & 1, abort))) break;
-          mbar_expect_tx(&bar->full_kv[c & 1], SM::K + SM::V);
-          load(&mk, sk + (c & 1) * SM::K, DK, &bar->full_kv[c & 1], ps.ck, c);
-          load(&mv, sv + (c & 1) * SM::V, DV, &bar->full_kv[c & 1], ps.cv, c);
-          ++kv_loads;
+        if (!la_wait(&bar->o1, c & 1, abort)) break;
+        load_q(c + 1);
+        if (!la_wait(&bar->staged[c & 1], ph, abort)) break;
+        if (tokens(c) == LC) {  // (the rows of a partial chunk are written by the math warps)
+          for (int x = 0; x < DV; x += 64)
+            tma_store_4d(&mo, sv + (c & 1) * SM::V + (x >> 6) * LA_BLOCK, x, tile_t(c), h * ps.co.h, b * ps.co.b);
+          bulk_commit();
+          bulk_wait_read();
         }
+        load_v(c + 2);
       }
+      bulk_wait_all();
     }
   } else if (warp == 1) {
     if (lane == 0 && chunks > 0) {
@@ -217,7 +265,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const uint32_t q0 = smem_u32(sq), e0 = smem_u32(se);
       bool ok = !(ps.stall && !la_wait(&bar->stall, 0, abort));
       for (int c = 0; c < chunks && ok; ++c) {
-        const uint32_t ph = c & 1;
+        const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
         const uint32_t k0 = smem_u32(sk + ph * SM::K), v0 = smem_u32(sv + ph * SM::V);
         auto u_piece = [&](uint32_t at, bool first) {
 #pragma unroll
@@ -225,11 +273,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             umma_bf16_ta(tmem + TM_U, tmem + at + kk * 8, sdesc_mn_sw128(v0 + kk * 2048, LA_BLOCK), id_v,
                          (first && kk == 0) ? 0u : 1u);
         };
-        if (!(ok = la_wait(&bar->full_kv[ph], (c >> 1) & 1, abort))) break;
         const bool state = init != nullptr || c > 0;
+        ok = la_wait(&bar->full_k[ph], ph2, abort) && la_wait(&bar->full_v[ph], ph2, abort) &&
+             la_wait(&bar->kt, ph, abort);
+        if (!ok) break;
+        tc_fence_after();
+        u_piece(TM_K0, true);
+        u_piece(TM_K1, false);
+        umma_commit(three ? &bar->u1 : &bar->u2);
         if (!local) {
-          if (!(ok = la_wait(&bar->full_q, ph, abort))) break;
-          if (c > 0 && !(ok = la_wait(&bar->o2[ph ^ 1], ((c - 1) >> 1) & 1, abort))) break;
+          ok = la_wait(&bar->full_q, ph, abort) &&
+               (c == 0 || la_wait(&bar->o2[ph ^ 1], ((c - 1) >> 1) & 1, abort));  // P's columns are free
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk) {
@@ -237,126 +292,209 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             umma_bf16(tmem + TM_P, sdesc_k_sw128(q0 + o), sdesc_k_sw128(k0 + o), id_p, kk != 0 ? 1u : 0u);
           }
           umma_commit(&bar->p);
-          if (!(ok = la_wait(&bar->next, ph, abort))) break;
-          tc_fence_after();
-          if (state) {
-#pragma unroll
-            for (int pc = 0; pc < 2; ++pc)
-#pragma unroll
-              for (int kk = 0; kk < DK / 16; ++kk)
-                umma_bf16(tmem + TM_O, sdesc_k_sw128(q0 + (kk >> 2) * LA_BLOCK + (kk & 3) * 32),
-                          sdesc_mn_sw128(e0 + pc * SM::E + kk * 2048, DK * 128), id_v, (pc | kk) != 0 ? 1u : 0u);
-          }
-          umma_commit(&bar->o1);
+          umma_commit(&bar->free_k[ph]);
         }
-        if (!(ok = la_wait(&bar->kt, ph, abort))) break;
+        if (three) {
+          if (!(ok = la_wait(&bar->khi, ph, abort))) break;
+          tc_fence_after();
+          u_piece(TM_K0, false);
+          umma_commit(&bar->u2);
+        }
+        if (local) {
+          umma_commit(&bar->free_k[ph]);  // K and V
+          continue;
+        }
+        if (!(ok = la_wait(&bar->next, ph, abort))) break;
         tc_fence_after();
-        u_piece(TM_K0, true);
-        u_piece(TM_K1, false);
-        umma_commit(&bar->u1);
+        if (state) {
+#pragma unroll
+          for (int pc = 0; pc < 2; ++pc)
+#pragma unroll
+            for (int kk = 0; kk < DK / 16; ++kk)
+              umma_bf16(tmem + TM_O, sdesc_k_sw128(q0 + (kk >> 2) * LA_BLOCK + (kk & 3) * 32),
+                        sdesc_mn_sw128(e0 + pc * SM::E + kk * 2048, DK * 128), id_v, (pc | kk) != 0 ? 1u : 0u);
+        }
+        umma_commit(&bar->o1);  // also: Q and E's pieces have been read
         if (!(ok = la_wait(&bar->mid, ph, abort))) break;
         tc_fence_after();
-        u_piece(TM_K0, false);
-        umma_commit(&bar->u2);
-        if (!local) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
+        for (int gq = 0; gq < 8; ++gq)   // 16 tokens: hi pieces in 8 columns, then lo
 #pragma unroll
-            for (int pc = 0; pc < 2; ++pc)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16_ta(tmem + TM_O, tmem + TM_P + hf * 64 + pc * 32 + kk * 8,
-                             sdesc_mn_sw128(v0 + (hf * 4 + kk) * 2048, LA_BLOCK), id_v,
-                             (state || (hf | pc | kk) != 0) ? 1u : 0u);
-        }
-        umma_commit(&bar->o2[ph]);  // also: this chunk's K and V have been read
+          for (int pc = 0; pc < 2; ++pc)
+            umma_bf16_ta(tmem + TM_O, tmem + TM_P + gq * 16 + pc * 8, sdesc_mn_sw128(v0 + gq * 2048, LA_BLOCK), id_v,
+                         (state || (gq | pc) != 0) ? 1u : 0u);
+        umma_commit(&bar->o2[ph]);
       }
       umma_commit(&bar->drain);  // completes once every MMA issued above has finished
       drain_wait(&bar->drain, 0);
     }
-  } else {
+  } else if (warp >= LA_ROLE_WARPS) {
     // ---------------- elementwise work ----------------
-    const int quad = warp & 3, hf = (warp - 2) >> 2;
+    regs_inc<LA_MATH_REGS>();
+    const int quad = warp & 3, cg = (warp - LA_ROLE_WARPS) >> 2;
     const int row = quad * 32 + lane;               // TMEM lane: token row, or state row
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    constexpr int EC = DV / 2;                      // columns of the state and of O per thread
-    const int j0 = hf * EC;
-    const int mt = threadIdx.x - 64;                // 0 .. 255
-    for (int j = mt; j <= LC; j += LA_MATH_WARPS * 32) pw[j] = decay_pow(ld, (float)j);
+    constexpr int EC = DV / 4;                      // columns of the state and of O per thread
+    constexpr int MT = LA_MATH_WARPS * 32;
+    const int j0 = cg * EC;
+    const int mt = threadIdx.x - LA_ROLE_WARPS * 32;
+    auto math_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(MT) : "memory"); };
+    if (mt <= LC) {
+      pw[mt] = decay_pow(ld, (float)mt);
+      if (mt < LC) bw[mt] = decay_pow(ld, (float)(a.reverse ? mt : LC - 1 - mt));
+    }
+    // what multiplies a finished row of O
+    const float r_out = fast ? a.out_scale * expf(ld * (float)(a.reverse ? -row : row - (LC - 1))) : a.out_scale;
 
+    // States in global memory go through the room of E's pieces when their rows are contiguous
+    // (fp32 d x DV, 16-byte chunks swizzled by row: a thread's own row directly would touch 32
+    // rows per access); transposed ones are contiguous across the lanes.
     float S[EC];
 #pragma unroll
     for (int j = 0; j < EC; ++j) S[j] = 0.f;
-    if (init && row < a.d) {
+    constexpr int CH = DV / 4;
+    auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(se + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
+    if (init) {
+      if (isj == 1 && (a.dv & 3) == 0 && ((uintptr_t)init & 15) == 0 && (isi & 3) == 0) {
+        for (int x = mt; x < a.d * CH; x += MT) {
+          const int r = x / CH, ch = x - r * CH;
+          *chunk_at(r, ch) = 4 * ch < a.dv ? *reinterpret_cast<const float4*>(init + r * isi + 4 * ch)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        math_sync();
+        if (row < a.d) {
 #pragma unroll
-      for (int j = 0; j < EC; ++j)
-        if (j0 + j < a.dv) S[j] = init[row * isi + (j0 + j) * isj] * in_scale;
+          for (int j = 0; j < EC; j += 4) {
+            const float4 x = *chunk_at(row, (j0 + j) >> 2);
+            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+          }
+        }
+      } else if (row < a.d) {
+#pragma unroll
+        for (int j = 0; j < EC; ++j)
+          if (j0 + j < a.dv) S[j] = init[row * isi + (j0 + j) * isj];
+      }
+#pragma unroll
+      for (int j = 0; j < EC; ++j) S[j] *= in_scale;
     }
-    auto put_state = [&]() {  // E as two bf16 pieces, the second operand of Q E
+    auto put_state = [&](float f) {  // f E as two bf16 pieces, the second operand of Q E
       if (row < DK) {
 #pragma unroll
         for (int j = 0; j < EC; j += 8) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            hi[u] = pack_bf16(S[j + 2 * u], S[j + 2 * u + 1]);
-            lo[u] = pack_bf16(S[j + 2 * u] - low_f(hi[u]), S[j + 2 * u + 1] - high_f(hi[u]));
+            float x0 = S[j + 2 * u], x1 = S[j + 2 * u + 1];
+            mul2(x0, x1, f, f);
+            hi[u] = pack_high(x0, x1);
+            below_high(x0, x1);
+            lo[u] = pack_bf16(x0, x1);
           }
           const uint32_t o = sw_off(row, j0 + j, DK);
           *reinterpret_cast<uint4*>(se + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(se + SM::E + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      fence_async_smem();
     };
-    if (init) put_state();
-    // the decay table is shared by the math warps only
-    asm volatile("bar.sync 1, %0;" ::"n"(LA_MATH_WARPS * 32) : "memory");
-    if (lane == 0) mbar_arrive(&bar->next);
+    auto head_ready = [&](int c) { return c == 0 && g == 0 && a.in_ready; };
+    math_sync();  // the decay tables; the staged state has been read
+    if (init) put_state(fast ? pw[LC - (head_ready(0) ? 1 : 0)] : 1.f);
+    float wk[8];  // weights of this thread's tokens in the transposed keys
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      wk[2 * i] = bw[cg * 32 + i * 8 + 2 * (lane & 3)];
+      wk[2 * i + 1] = bw[cg * 32 + i * 8 + 2 * (lane & 3) + 1];
+    }
+    const uint32_t k_at = (uint32_t)((quad >> 1) * LA_BLOCK + (cg * 32 + (lane & 7)) * 128 +
+                                     ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
 
-    const char* const op = (const char*)a.o.p + ((long long)b * a.o.sb + (long long)h * a.o.sh) * 2;
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t ph = c & 1;
-      const int m = min(LC, t1 - t0 - c * LC);      // tokens of this chunk
-      const int r0 = a.reverse ? LC - m : 0;        // their rows: [r0, r0 + m)
-      const bool ready = c == 0 && g == 0 && a.in_ready;
-      if (!la_wait_warp(&bar->full_kv[ph], (c >> 1) & 1, abort, lane)) break;
-      const uint8_t* kt = sk + ph * SM::K;
-      uint8_t* vt = sv + ph * SM::V;
-
-      // weighted keys a^(m-1-s) k_s, transposed: thread = state row, 64 of the tokens
-      uint32_t khi[32];
+    // O of chunk c, whose products have finished, leaves
+    auto put_out = [&](int c) {
+      const int m = tokens(c), r0 = a.reverse ? LC - m : 0;
+      uint8_t* vt = sv + (c & 1) * SM::V;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t md[16], lo[16];
+      for (int q = 0; q < EC; q += 16) {
+        uint32_t v[16], y[8];
+        tmem_ld16(lanes + TM_O + j0 + q, v);
+        tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int s = hf * 64 + q * 32 + 2 * i + u;
-            const int e = a.reverse ? s - r0 : m - 1 - s;   // exponent; < 0 outside the chunk
-            float kv = 0.f;
-            if (DK == 128 || row < DK)
-              kv = __uint_as_float((uint32_t)(*reinterpret_cast<const uint16_t*>(kt + sw_off(s, row, LC))) << 16);
-            x[u] = e >= 0 ? kv * pw[e < 0 ? 0 : e] : 0.f;
-          }
-          const uint32_t hi = pack_bf16(x[0], x[1]);
-          khi[q * 16 + i] = hi;
-          x[0] -= low_f(hi);
-          x[1] -= high_f(hi);
-          md[i] = pack_bf16(x[0], x[1]);
-          lo[i] = pack_bf16(x[0] - low_f(md[i]), x[1] - high_f(md[i]));
+        for (int u = 0; u < 8; ++u) {
+          float x0 = __uint_as_float(v[2 * u]), x1 = __uint_as_float(v[2 * u + 1]);
+          mul2(x0, x1, r_out, r_out);
+          y[u] = pack_bf16(x0, x1);
         }
-        tmem_st16(lanes + TM_K0 + hf * 32 + q * 16, lo);
-        tmem_st16(lanes + TM_K1 + hf * 32 + q * 16, md);
+        const int j = j0 + q;
+        if (m == LC) {
+          *reinterpret_cast<uint4*>(vt + sw_off(row, j, LC)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(vt + sw_off(row, j + 8, LC)) = make_uint4(y[4], y[5], y[6], y[7]);
+        } else if (row >= r0 && row < r0 + m) {
+          const long long t = (long long)tile_t(c) + row;
+          char* dst = (char*)a.o.p + ((long long)b * a.o.sb + (long long)h * a.o.sh + t * a.o.st + j) * 2;
+          if (j < a.dv) *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (j + 8 < a.dv) *reinterpret_cast<uint4*>(dst + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->staged[c & 1]);
+    };
+
+    int c = 0;
+    for (; c < chunks; ++c) {
+      const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
+      const int m = tokens(c);
+      const int r0 = a.reverse ? LC - m : 0;        // the tokens' rows: [r0, r0 + m)
+      if (!la_wait_warp(&bar->full_k[ph], ph2, abort)) break;
+
+      // weighted keys a^(m-1-s) k_s, transposed: 32 state rows x 32 tokens per warp
+      uint32_t khi[2][8];
+      {
+        const uint32_t kt = smem_u32(sk + ph * SM::K) + k_at;
+        uint32_t md[2][8], lo[2][8];
+#pragma unroll
+        for (int sb = 0; sb < 4; ++sb) {
+          uint32_t x4[4] = {0u, 0u, 0u, 0u};
+          if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + sb * 1024, x4);
+          float w0 = wk[2 * sb], w1 = wk[2 * sb + 1];
+          if (m < LC) {
+            const int s = cg * 32 + sb * 8 + 2 * (lane & 3);
+            const int e = a.reverse ? s - r0 : m - 1 - s, e1 = a.reverse ? e + 1 : e - 1;
+            const uint32_t keep = (e >= 0 ? 0xffffu : 0u) | (e1 >= 0 ? 0xffff0000u : 0u);  // not NaN times 0
+            w0 = pw[e < 0 ? 0 : e];
+            w1 = pw[e1 < 0 ? 0 : e1];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x4[u] &= keep;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x0 = __uint_as_float(x4[u] << 16), x1 = __uint_as_float(x4[u] & 0xffff0000u);
+            mul2(x0, x1, w0, w1);
+            const int at = sb * 2 + (u & 1);
+            khi[u >> 1][at] = pack_high(x0, x1);
+            below_high(x0, x1);
+            if (three) {
+              md[u >> 1][at] = pack_high(x0, x1);
+              below_high(x0, x1);
+            }
+            lo[u >> 1][at] = pack_bf16(x0, x1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + cg * 16;
+          tmem_st_16x128_x4(at + TM_K0, lo[u]);
+          if (three) tmem_st_16x128_x4(at + TM_K1, md[u]);
+          else tmem_st_16x128_x4(at + TM_K1, khi[u]);
+        }
       }
       if (m < LC && !a.reverse) {
         // rows behind the sequence's end may hold anything, NaN included, which a weight of
-        // zero does not remove: V's rows are cleared (the weights above drop K's)
-        for (int x = mt; x < (LC - m) * (DV / 8); x += LA_MATH_WARPS * 32) {
+        // zero does not remove: V's rows are cleared
+        if (!la_wait_warp(&bar->full_v[ph], ph2, abort)) break;
+        for (int x = mt; x < (LC - m) * (DV / 8); x += MT) {
           const int r = m + x / (DV / 8), cj = (x % (DV / 8)) * 8;
-          *reinterpret_cast<uint4*>(vt + sw_off(r, cj, LC)) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sv + ph * SM::V + sw_off(r, cj, LC)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();
       }
@@ -366,111 +504,146 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       if (lane == 0) mbar_arrive(&bar->kt);
 
       if (!local) {
-        // P pieces in place: thread = token row, 64 of the columns
-        if (!la_wait_warp(&bar->p, ph, abort, lane)) break;
-        tc_fence_after();
-        uint32_t hi[32], lo[32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-          tmem_ld32(lanes + TM_P + hf * 64 + q * 32, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int s = hf * 64 + q * 32 + 2 * i + u;
-              const int e = a.reverse ? s - row : row - s;
-              x[u] = e >= 0 ? __uint_as_float(v[2 * i + u]) * pw[e < 0 ? 0 : e] : 0.f;
-            }
-            hi[q * 16 + i] = pack_bf16(x[0], x[1]);
-            lo[q * 16 + i] = pack_bf16(x[0] - low_f(hi[q * 16 + i]), x[1] - high_f(hi[q * 16 + i]));
-          }
-        }
-        tmem_st32(lanes + TM_P + hf * 64, hi);
-        tmem_st32(lanes + TM_P + hf * 64 + 32, lo);
-        // O = Q E so far: decay each token's row
-        if (init != nullptr || c > 0) {
-          if (!la_wait_warp(&bar->o1, ph, abort, lane)) break;
+        if (c > 0) {
+          // E's pieces (the previous chunk's have been read) and the previous chunk's rows of O
+          if (!la_wait_warp(&bar->o1, (c - 1) & 1, abort)) break;
+          put_state(fast ? pw[LC] : 1.f);
+          if (!la_wait_warp(&bar->o2[(c - 1) & 1], ((c - 1) >> 1) & 1, abort)) break;
           tc_fence_after();
-          const int u = a.reverse ? LC - 1 - row : row;
-          const float f = pw[u + (ready ? 0 : 1)];
-#pragma unroll
-          for (int q = 0; q < EC; q += 32) {
-            uint32_t v[32];
-            tmem_ld32(lanes + TM_O + j0 + q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st32(lanes + TM_O + j0 + q, v);
-          }
+          put_out(c - 1);
+        } else {
+          fence_async_smem();  // the first pieces
+          __syncwarp();
         }
+        if (lane == 0) mbar_arrive(&bar->next);
       }
-      // the keys' high piece takes the low one's place once that has been read
-      if (!la_wait_warp(&bar->u1, ph, abort, lane)) break;
-      tc_fence_after();
-      tmem_st32(lanes + TM_K0 + hf * 32, khi);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->mid);
-
-      // E' = a^len E + U
-      if (!la_wait_warp(&bar->u2, ph, abort, lane)) break;
-      tc_fence_after();
-      {
-        const float e = (float)(m - (ready ? 1 : 0));
-        const float fhi = decay_pow(ld, e);
-#pragma unroll
-        for (int q = 0; q < EC; q += 32) {
-          uint32_t v[32];
-          tmem_ld32(lanes + TM_U + j0 + q, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) S[q + i] = fmaf(S[q + i], fhi, __uint_as_float(v[i]));
-        }
-      }
-      if (!local) {
-        if (c + 1 < chunks) put_state();
-        if (!la_wait_warp(&bar->o2[ph], (c >> 1) & 1, abort, lane)) break;
+      if (three) {
+        // the keys' high piece takes the low one's place once that has been read
+        if (!la_wait_warp(&bar->u1, ph, abort)) break;
         tc_fence_after();
-        const long long t = tile_t(c) + row;
-        char* dst = const_cast<char*>(op) + t * a.o.st * 2;
-        const bool live = row >= r0 && row < r0 + m;
 #pragma unroll
-        for (int q = 0; q < EC; q += 32) {
-          uint32_t v[32];
-          tmem_ld32(lanes + TM_O + j0 + q, v);
-          tmem_wait_ld();
-          if (live) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              if (j0 + q + i < a.dv) {
-                uint32_t y[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  y[u] = pack_bf16(__uint_as_float(v[i + 2 * u]) * a.out_scale,
-                                   __uint_as_float(v[i + 2 * u + 1]) * a.out_scale);
-                *reinterpret_cast<uint4*>(dst + (j0 + q + i) * 2) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            }
-          }
-        }
+        for (int u = 0; u < 2; ++u) tmem_st_16x128_x4(lanes + ((uint32_t)(u * 16) << 16) + cg * 16 + TM_K0, khi[u]);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->next);
+        if (lane == 0) mbar_arrive(&bar->khi);
+      }
+      if (!local) {
+        // P pieces in place, 16 columns (8 of hi, 8 of lo) at a time: thread = token row.
+        // The warp's 32 x 32 block is behind the tokens, ahead of them (zero), or on the diagonal.
+        if (!la_wait_warp(&bar->p, ph, abort)) break;
+        tc_fence_after();
+        const int dq = a.reverse ? cg - quad : quad - cg;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int s0 = cg * 32 + q * 16;
+          uint32_t pc[16];
+          if (dq < 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pc[i] = 0u;
+          } else {
+            uint32_t v[16];
+            tmem_ld16(lanes + TM_P + s0, v);
+            tmem_wait_ld();
+            if (fast) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(bw + s0 + i);
+                float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
+                float x2 = __uint_as_float(v[i + 2]), x3 = __uint_as_float(v[i + 3]);
+                mul2(x0, x1, w.x, w.y);
+                mul2(x2, x3, w.z, w.w);
+                v[i] = __float_as_uint(x0); v[i + 1] = __float_as_uint(x1);
+                v[i + 2] = __float_as_uint(x2); v[i + 3] = __float_as_uint(x3);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int e = a.reverse ? s0 + i - row : row - s0 - i;
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * pw[e < 0 ? 0 : e]);
+              }
+            }
+            if (dq == 0) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (a.reverse ? q * 16 + i < lane : q * 16 + i > lane) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x0 = __uint_as_float(v[2 * i]), x1 = __uint_as_float(v[2 * i + 1]);
+              pc[i] = pack_high(x0, x1);
+              below_high(x0, x1);
+              pc[8 + i] = pack_bf16(x0, x1);
+            }
+          }
+          tmem_st16(lanes + TM_P + s0, pc);
+        }
+        if (!fast && (init != nullptr || c > 0)) {
+          // O = Q E so far: decay each token's row
+          if (!la_wait_warp(&bar->o1, ph, abort)) break;
+          tc_fence_after();
+          const int u = a.reverse ? LC - 1 - row : row;
+          const float f = pw[u + (head_ready(c) ? 0 : 1)];
+#pragma unroll
+          for (int q = 0; q < EC; q += 16) {
+            uint32_t v[16];
+            tmem_ld16(lanes + TM_O + j0 + q, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st16(lanes + TM_O + j0 + q, v);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->mid);
+      }
+
+      // E' = a^len E + U
+      if (!la_wait_warp(&bar->u2, ph, abort)) break;
+      tc_fence_after();
+      {
+        const float f = pw[m - (head_ready(c) ? 1 : 0)];
+#pragma unroll
+        for (int q = 0; q < EC; q += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + TM_U + j0 + q, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 2)
+            fma2(S[q + i], S[q + i + 1], f, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        }
+      }
+    }
+    if (!local && chunks > 0 && c == chunks) {
+      if (la_wait_warp(&bar->o2[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, abort)) {
+        tc_fence_after();
+        put_out(chunks - 1);
       }
     }
     // last state: the segment's slot, or the caller's
     float* dst = local ? a.slots + ((size_t)bh * a.nseg + g) * cells
                        : (a.s_out && g == a.nseg - 1 ? a.s_out + (size_t)bh * cells : nullptr);
-    if (dst && row < a.d && !*abort) {
+    if (dst) {
       const long long osi = local ? a.dv : a.si, osj = local ? 1 : a.sj;
       const float w = local || n == 0 ? 1.f : a.st_scale * (a.out_decay ? decay_pow(ld, 1.f) : 1.f);
+      if (osj == 1 && (a.dv & 3) == 0 && ((uintptr_t)dst & 15) == 0 && (osi & 3) == 0) {
+        if (row < a.d) {  // every product that read E's pieces has finished
 #pragma unroll
-      for (int j = 0; j < EC; ++j)
-        if (j0 + j < a.dv) dst[row * osi + (j0 + j) * osj] = S[j] * w;
+          for (int j = 0; j < EC; j += 4)
+            *chunk_at(row, (j0 + j) >> 2) = make_float4(S[j] * w, S[j + 1] * w, S[j + 2] * w, S[j + 3] * w);
+        }
+        math_sync();
+        for (int x = mt; x < a.d * CH; x += MT) {
+          const int r = x / CH, ch = x - r * CH;
+          if (4 * ch < a.dv && !*abort) *reinterpret_cast<float4*>(dst + r * osi + 4 * ch) = *chunk_at(r, ch);
+        }
+      } else if (row < a.d && !*abort) {
+#pragma unroll
+        for (int j = 0; j < EC; ++j)
+          if (j0 + j < a.dv) dst[row * osi + (j0 + j) * osj] = S[j] * w;
+      }
     }
   }
 
@@ -478,7 +651,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   __syncwarp();
   if (warp == 0 && lane == 0 && *abort) {
     // let the copies this CTA issued land before its shared memory goes away
-    for (int c = kv_loads < 2 ? 0 : kv_loads - 2; c < kv_loads; ++c) drain_wait(&bar->full_kv[c & 1], (c >> 1) & 1);
+    for (int i = k_loads < 2 ? 0 : k_loads - 2; i < k_loads; ++i) drain_wait(&bar->full_k[i & 1], (i >> 1) & 1);
+    for (int i = v_loads < 2 ? 0 : v_loads - 2; i < v_loads; ++i) drain_wait(&bar->full_v[i & 1], (i >> 1) & 1);
     if (q_loads > 0) drain_wait(&bar->full_q, (q_loads - 1) & 1);
   }
   tc_fence_before();
@@ -532,16 +706,18 @@ bool grid16(const fwpkm_heads& x, const ScanArgs& a) {
 }
 
 template <int DK, int DV>
-int go_tc(const TcPass& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+int go_tc(const TcPass& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+          cudaStream_t s) {
   if (!raise_smem_limit((const void*)scan_tc_kernel<DK, DV>, TcSmem<DK, DV>::bytes)) return -1;
   launch_k(scan_tc_kernel<DK, DV>, dim3((unsigned)(p.a.B * p.a.H), p.local ? p.a.nseg - 1 : p.a.nseg), LA_THREADS,
-           TcSmem<DK, DV>::bytes, s, q, k, v, p);
+           TcSmem<DK, DV>::bytes, s, q, k, v, o, p);
   return 1;
 }
 
-int go_tc_shape(const TcPass& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
-  if (p.a.d <= 64) return p.a.dv <= 64 ? go_tc<64, 64>(p, q, k, v, s) : go_tc<64, 128>(p, q, k, v, s);
-  return p.a.dv <= 64 ? go_tc<128, 64>(p, q, k, v, s) : go_tc<128, 128>(p, q, k, v, s);
+int go_tc_shape(const TcPass& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+          cudaStream_t s) {
+  if (p.a.d <= 64) return p.a.dv <= 64 ? go_tc<64, 64>(p, q, k, v, o, s) : go_tc<64, 128>(p, q, k, v, o, s);
+  return p.a.dv <= 64 ? go_tc<128, 64>(p, q, k, v, o, s) : go_tc<128, 128>(p, q, k, v, o, s);
 }
 
 }  // namespace
@@ -571,9 +747,9 @@ int launch_scan_tc(const ScanArgs& a0, cudaStream_t s) {
   p.a = a0;
   p.a.nseg = scan_tc_segments(a0);
   p.a.seg_len = p.a.nseg > 1 ? ((a0.T + p.a.nseg - 1) / p.a.nseg + LC - 1) / LC * LC : a0.T;
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   if (!heads_map(&q, a0.q, a0, a0.d, &p.cq) || !heads_map(&k, a0.k, a0, a0.d, &p.ck) ||
-      !heads_map(&v, a0.v, a0, a0.dv, &p.cv)) {
+      !heads_map(&v, a0.v, a0, a0.dv, &p.cv) || !heads_map(&o, a0.o, a0, a0.dv, &p.co)) {
     fprintf(stderr, "fwpkm: cuTensorMapEncodeTiled failed\n");
     return -1;
   }
@@ -581,12 +757,12 @@ int launch_scan_tc(const ScanArgs& a0, cudaStream_t s) {
   p.stall = take_test_stall();
   if (p.a.nseg > 1) {
     p.local = 1;
-    if (go_tc_shape(p, q, k, v, s) < 0) return -1;
+    if (go_tc_shape(p, q, k, v, o, s) < 0) return -1;
     nl += 1 + launch_scan_combine(p.a, s);
     p.local = 0;
     p.stall = 0;
   }
-  if (go_tc_shape(p, q, k, v, s) < 0) return -1;
+  if (go_tc_shape(p, q, k, v, o, s) < 0) return -1;
   return nl + 1;
 }
 
