@@ -23,14 +23,17 @@
 //
 // CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one;
 // the rows of O leave through V's stage), warp 1 owns TMEM and issues the MMAs (one thread),
-// warps 4-19 do the elementwise work: warp w reads TMEM lanes 32 (w % 4).. and column group
-// (w - 4) / 4.  TMEM (512 columns): P fp32, overwritten in place by its two bf16 pieces
-// (operand A of P V); O; U; two pieces of the weighted, transposed keys (operand A of U; the
-// high piece waits in registers and takes the low one's place).  Per chunk c, in order:
-//   MMA    U lo, mid(c)    P(c)        U hi(c)     Q E(c)               P V(c)
-//   math   E pieces(c-1), O out(c-1)   K hi        P pieces(c)    E(c)  K pieces(c+1)
+// warps 4-11 carry the state, warps 12-19 the scores and the output: a warp reads TMEM lanes
+// 32 (w % 4).. and one half of the columns.  TMEM (512 columns): P fp32, overwritten in place
+// by its two bf16 pieces (operand A of P V); O; U; two pieces of the weighted, transposed keys
+// (operand A of U; the high piece waits in registers and takes the low one's place).
+// Per chunk c, in order:
+//   MMA     U lo, mid(c)   P(c)   U hi(c)        Q E(c)               P V(c)
+//   state         K hi(c)              E(c), K pieces(c+1), E pieces(c+1)
+//   scores  O out(c-1)                 P pieces(c)
 // so the MMAs of a chunk (8 products of 128^3, 4096 cycles at the dense rate) follow one another
-// while the elementwise work is done beside them.
+// while both groups work beside them.  (With all sixteen warps doing everything in turn, a
+// chunk took the sum of the steps' latencies: 5.5 us.)
 // Bound: HBM for d = d_v = 128 (128 KB per chunk, 5500 cycles of an SM's share at 6.46 TB/s).
 #include <cstdio>
 
@@ -44,14 +47,14 @@ using namespace sm100;
 namespace {
 
 constexpr int LC = 128;                  // tokens per chunk
-// Four warps of roles (two idle: register shares go by warpgroups) and sixteen of elementwise
-// work, four per scheduler: with eight the kernel waited on latency (0.24 instructions per
-// cycle and scheduler).  640 threads launch at 96 registers; the roles give theirs up for the
-// others: 128 x 64 + 512 x 104 = 61440 = 640 x 96.
-constexpr int LA_ROLE_WARPS = 4, LA_MATH_WARPS = 16;
-constexpr int LA_THREADS = (LA_ROLE_WARPS + LA_MATH_WARPS) * 32;
-constexpr int LA_ROLE_REGS = 64, LA_MATH_REGS = 104;
-static_assert(LA_ROLE_WARPS * 32 * LA_ROLE_REGS + LA_MATH_WARPS * 32 * LA_MATH_REGS <= LA_THREADS * 96, "registers");
+// Warps by warpgroup (register shares go by warpgroups): four of roles (two idle), eight that
+// carry the state (weighted keys, E), eight for the scores and the output.  640 threads launch
+// at 96 registers and redistribute them.
+constexpr int LA_ROLE_WARPS = 4, LA_ST_WARPS = 8, LA_PO_WARPS = 8;
+constexpr int LA_THREADS = (LA_ROLE_WARPS + LA_ST_WARPS + LA_PO_WARPS) * 32;
+constexpr int LA_ROLE_REGS = 48, LA_ST_REGS = 136, LA_PO_REGS = 80;
+static_assert(32 * (LA_ROLE_WARPS * LA_ROLE_REGS + LA_ST_WARPS * LA_ST_REGS + LA_PO_WARPS * LA_PO_REGS) <=
+                  LA_THREADS * 96, "registers");
 constexpr uint64_t LA_TIMEOUT_NS = 200ull * 1000 * 1000;  // any single wait
 constexpr float LA_RANGE = 60.f;         // largest |log a^128| taken through column weights
 constexpr int LA_BLOCK = LC * 128;       // bytes of a 64-column block of 128 rows
@@ -63,14 +66,14 @@ constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_K1 = 448, T
 
 struct TcBars {
   uint64_t full_q, full_k[2], full_v[2], free_k[2], staged[2], o2[2];
-  uint64_t p, o1, kt, khi, u1, mid, u2, next, drain, stall;
+  uint64_t p, o1, kt, khi, u1, mid, u2, est, ofree, cleared, drain, stall;
 };
 
 template <int DK, int DV>
 struct TcSmem {
   static constexpr int Q = LC * DK * 2, K = LC * DK * 2, V = LC * DV * 2, E = DK * DV * 2;
   static constexpr int off_k = Q, off_v = off_k + 2 * K, off_e = off_v + 2 * V, off_tab = off_e + 2 * E;
-  static constexpr int need = off_tab + 4 * (2 * LC + 4) + (int)sizeof(TcBars) + 16 + 1024;
+  static constexpr int need = off_tab + 4 * (3 * LC + 4) + (int)sizeof(TcBars) + 16 + 1024;
   // one CTA per SM: each holds all of TMEM
   static constexpr int bytes = need > 120 * 1024 ? need : 120 * 1024;
 };
@@ -79,12 +82,12 @@ struct TcSmem {
 __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   uint32_t n = 0;
   uint64_t t0 = 0;
+#pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
     if ((++n & 255u) == 0) {
-      if (*abort) return false;
       const uint64_t t = globaltimer();
       if (t0 == 0) t0 = t;
-      else if (t - t0 > LA_TIMEOUT_NS) {
+      if (*abort || t - t0 > LA_TIMEOUT_NS) {
         *abort = 1;
         return false;
       }
@@ -95,6 +98,15 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, volatile
 // The same for a whole warp, converged afterwards: true only if every lane saw the phase.
 __device__ __forceinline__ bool la_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, la_wait(bar, parity, abort)) != 0;
+}
+// Several waits at once by a converged warp: lane i < n waits for the i-th (bar, parity).
+struct Wait {
+  uint64_t* bar;
+  uint32_t parity;
+};
+__device__ __forceinline__ bool la_wait_each(int lane, volatile int* abort, Wait a, Wait b, Wait c) {
+  const Wait w = lane == 0 ? a : lane == 1 ? b : c;
+  return __all_sync(0xffffffffu, la_wait(w.bar, w.parity, abort)) != 0;
 }
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
@@ -138,7 +150,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sq = smem, *sk = smem + SM::off_k, *sv = smem + SM::off_v, *se = smem + SM::off_e;
   float* bw = (float*)(smem + SM::off_tab);  // [LC] column weights B_s
-  float* pw = bw + LC;                       // [LC + 1] a^j
+  float* kw = bw + LC;                       // [LC] weights of the chunk's keys
+  float* pw = kw + LC;                       // [LC + 1] a^j
   TcBars* bar = (TcBars*)(pw + LC + 4);
   uint32_t* tmem_slot = (uint32_t*)(bar + 1);
   volatile int* abort = (volatile int*)(tmem_slot + 1);
@@ -156,17 +169,19 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       mbar_init(&bar->full_k[i], 1);
       mbar_init(&bar->full_v[i], 1);
       mbar_init(&bar->free_k[i], 1);
-      mbar_init(&bar->staged[i], LA_MATH_WARPS);
+      mbar_init(&bar->staged[i], LA_PO_WARPS);
       mbar_init(&bar->o2[i], 1);
     }
     mbar_init(&bar->p, 1);
     mbar_init(&bar->o1, 1);
-    mbar_init(&bar->kt, LA_MATH_WARPS);
-    mbar_init(&bar->khi, LA_MATH_WARPS);
+    mbar_init(&bar->kt, LA_ST_WARPS);
+    mbar_init(&bar->khi, LA_ST_WARPS);
     mbar_init(&bar->u1, 1);
-    mbar_init(&bar->mid, LA_MATH_WARPS);
+    mbar_init(&bar->mid, LA_PO_WARPS);
     mbar_init(&bar->u2, 1);
-    mbar_init(&bar->next, LA_MATH_WARPS);
+    mbar_init(&bar->est, LA_ST_WARPS);
+    mbar_init(&bar->ofree, LA_PO_WARPS);
+    mbar_init(&bar->cleared, LA_ST_WARPS);
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
     *abort = 0;
@@ -259,92 +274,111 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       bulk_wait_all();
     }
   } else if (warp == 1) {
-    if (lane == 0 && chunks > 0) {
-      // ---------------- MMA issuer ----------------
+    if (chunks > 0) {
+      // ---------------- MMA issuer: the warp waits together, one lane issues ----------------
       constexpr uint32_t id_p = idesc_bf16_f32(LC, LC), id_v = idesc_bf16_f32(LC, DV) | IDESC_B_MN;
       const uint32_t q0 = smem_u32(sq), e0 = smem_u32(se);
-      bool ok = !(ps.stall && !la_wait(&bar->stall, 0, abort));
+      bool ok = !(ps.stall && !la_wait_warp(&bar->stall, 0, abort));
       for (int c = 0; c < chunks && ok; ++c) {
         const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
         const uint32_t k0 = smem_u32(sk + ph * SM::K), v0 = smem_u32(sv + ph * SM::V);
+        const uint64_t vd = sdesc_mn_sw128(v0, LA_BLOCK);   // + 128 per 16 tokens (16-byte units)
         auto u_piece = [&](uint32_t at, bool first) {
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < LC / 16; ++kk)
-            umma_bf16_ta(tmem + TM_U, tmem + at + kk * 8, sdesc_mn_sw128(v0 + kk * 2048, LA_BLOCK), id_v,
-                         (first && kk == 0) ? 0u : 1u);
+            umma_bf16_ta(tmem + TM_U, tmem + at + kk * 8, vd + kk * 128, id_v, (first && kk == 0) ? 0u : 1u);
         };
         const bool state = init != nullptr || c > 0;
-        ok = la_wait(&bar->full_k[ph], ph2, abort) && la_wait(&bar->full_v[ph], ph2, abort) &&
-             la_wait(&bar->kt, ph, abort);
+        ok = la_wait_each(lane, abort, {&bar->kt, ph}, {&bar->full_v[ph], ph2}, {&bar->full_k[ph], ph2});
         if (!ok) break;
         tc_fence_after();
-        u_piece(TM_K0, true);
-        u_piece(TM_K1, false);
-        umma_commit(three ? &bar->u1 : &bar->u2);
+        if (elect_one()) {
+          u_piece(TM_K0, true);
+          u_piece(TM_K1, false);
+          umma_commit(three ? &bar->u1 : &bar->u2);
+        }
+        __syncwarp();
         if (!local) {
-          ok = la_wait(&bar->full_q, ph, abort) &&
-               (c == 0 || la_wait(&bar->o2[ph ^ 1], ((c - 1) >> 1) & 1, abort));  // P's columns are free
+          // (o2 of the chunk before: P's columns are free)
+          const Wait q{&bar->full_q, ph};
+          ok = la_wait_each(lane, abort, q, c == 0 ? q : Wait{&bar->o2[ph ^ 1], (uint32_t)(((c - 1) >> 1) & 1)}, q);
           if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {
+            const uint64_t qd = sdesc_k_sw128(q0), kd = sdesc_k_sw128(k0);
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * LA_BLOCK + (kk & 3) * 32;
-            umma_bf16(tmem + TM_P, sdesc_k_sw128(q0 + o), sdesc_k_sw128(k0 + o), id_p, kk != 0 ? 1u : 0u);
+            for (int x = 0; x < DK / 64; ++x)
+#pragma unroll 2
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem + TM_P, qd + x * (LA_BLOCK >> 4) + kk * 2, kd + x * (LA_BLOCK >> 4) + kk * 2, id_p,
+                          (x | kk) != 0 ? 1u : 0u);
+            umma_commit(&bar->p);
+            if (!three) umma_commit(&bar->free_k[ph]);
           }
-          umma_commit(&bar->p);
-          umma_commit(&bar->free_k[ph]);
+          __syncwarp();
         }
         if (three) {
-          if (!(ok = la_wait(&bar->khi, ph, abort))) break;
+          if (!(ok = la_wait_warp(&bar->khi, ph, abort))) break;
           tc_fence_after();
-          u_piece(TM_K0, false);
-          umma_commit(&bar->u2);
+          if (elect_one()) {
+            u_piece(TM_K0, false);
+            umma_commit(&bar->u2);
+            umma_commit(&bar->free_k[ph]);  // (the state warps re-read K for its high piece)
+          }
+          __syncwarp();
         }
         if (local) {
-          umma_commit(&bar->free_k[ph]);  // K and V
+          if (!three) {
+            if (elect_one()) umma_commit(&bar->free_k[ph]);
+            __syncwarp();
+          }
           continue;
         }
-        if (!(ok = la_wait(&bar->next, ph, abort))) break;
+        // E's pieces, and O's columns (the rows of the previous chunk have left)
+        const Wait est{&bar->est, ph};
+        ok = la_wait_each(lane, abort, est, c == 0 ? est : Wait{&bar->ofree, ph ^ 1}, est);
+        if (!ok) break;
         tc_fence_after();
-        if (state) {
-#pragma unroll
-          for (int pc = 0; pc < 2; ++pc)
-#pragma unroll
-            for (int kk = 0; kk < DK / 16; ++kk)
-              umma_bf16(tmem + TM_O, sdesc_k_sw128(q0 + (kk >> 2) * LA_BLOCK + (kk & 3) * 32),
-                        sdesc_mn_sw128(e0 + pc * SM::E + kk * 2048, DK * 128), id_v, (pc | kk) != 0 ? 1u : 0u);
+        if (elect_one()) {
+          if (state) {
+            const uint64_t qd = sdesc_k_sw128(q0), ed = sdesc_mn_sw128(e0, DK * 128);
+#pragma unroll 1
+            for (int pc = 0; pc < 2; ++pc)
+#pragma unroll 2
+              for (int kk = 0; kk < DK / 16; ++kk)
+                umma_bf16(tmem + TM_O, qd + (kk >> 2) * (LA_BLOCK >> 4) + (kk & 3) * 2,
+                          ed + pc * (SM::E >> 4) + kk * 128, id_v, (pc | kk) != 0 ? 1u : 0u);
+          }
+          umma_commit(&bar->o1);  // also: Q and E's pieces have been read
         }
-        umma_commit(&bar->o1);  // also: Q and E's pieces have been read
-        if (!(ok = la_wait(&bar->mid, ph, abort))) break;
+        __syncwarp();
+        if (!(ok = la_wait_warp(&bar->mid, ph, abort))) break;
         tc_fence_after();
-#pragma unroll
-        for (int gq = 0; gq < 8; ++gq)   // 16 tokens: hi pieces in 8 columns, then lo
-#pragma unroll
-          for (int pc = 0; pc < 2; ++pc)
-            umma_bf16_ta(tmem + TM_O, tmem + TM_P + gq * 16 + pc * 8, sdesc_mn_sw128(v0 + gq * 2048, LA_BLOCK), id_v,
-                         (state || (gq | pc) != 0) ? 1u : 0u);
-        umma_commit(&bar->o2[ph]);
+        if (elect_one()) {
+#pragma unroll 2
+          for (int gq = 0; gq < 8; ++gq) {  // 16 tokens: hi pieces in 8 columns, then lo
+            umma_bf16_ta(tmem + TM_O, tmem + TM_P + gq * 16, vd + gq * 128, id_v, (state || gq != 0) ? 1u : 0u);
+            umma_bf16_ta(tmem + TM_O, tmem + TM_P + gq * 16 + 8, vd + gq * 128, id_v, 1u);
+          }
+          umma_commit(&bar->o2[ph]);
+        }
+        __syncwarp();
       }
-      umma_commit(&bar->drain);  // completes once every MMA issued above has finished
+      if (elect_one()) umma_commit(&bar->drain);  // completes once every MMA issued above has finished
+      __syncwarp();
       drain_wait(&bar->drain, 0);
     }
-  } else if (warp >= LA_ROLE_WARPS) {
-    // ---------------- elementwise work ----------------
-    regs_inc<LA_MATH_REGS>();
-    const int quad = warp & 3, cg = (warp - LA_ROLE_WARPS) >> 2;
-    const int row = quad * 32 + lane;               // TMEM lane: token row, or state row
+  } else if (warp >= LA_ROLE_WARPS && warp < LA_ROLE_WARPS + LA_ST_WARPS) {
+    // ---------------- the state: weighted keys, E ----------------
+    regs_inc<LA_ST_REGS>();
+    const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS) >> 2;
+    const int row = quad * 32 + lane;               // TMEM lane: state row
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    constexpr int EC = DV / 4;                      // columns of the state and of O per thread
-    constexpr int MT = LA_MATH_WARPS * 32;
-    const int j0 = cg * EC;
+    constexpr int EC = DV / 2;                      // columns of the state per thread
+    constexpr int ST = LA_ST_WARPS * 32;
+    const int j0 = hf * EC;
     const int mt = threadIdx.x - LA_ROLE_WARPS * 32;
-    auto math_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(MT) : "memory"); };
-    if (mt <= LC) {
-      pw[mt] = decay_pow(ld, (float)mt);
-      if (mt < LC) bw[mt] = decay_pow(ld, (float)(a.reverse ? mt : LC - 1 - mt));
-    }
-    // what multiplies a finished row of O
-    const float r_out = fast ? a.out_scale * expf(ld * (float)(a.reverse ? -row : row - (LC - 1))) : a.out_scale;
+    auto st_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(ST) : "memory"); };
 
     // States in global memory go through the room of E's pieces when their rows are contiguous
     // (fp32 d x DV, 16-byte chunks swizzled by row: a thread's own row directly would touch 32
@@ -356,12 +390,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(se + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
     if (init) {
       if (isj == 1 && (a.dv & 3) == 0 && ((uintptr_t)init & 15) == 0 && (isi & 3) == 0) {
-        for (int x = mt; x < a.d * CH; x += MT) {
+        for (int x = mt; x < a.d * CH; x += ST) {
           const int r = x / CH, ch = x - r * CH;
           *chunk_at(r, ch) = 4 * ch < a.dv ? *reinterpret_cast<const float4*>(init + r * isi + 4 * ch)
                                            : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        math_sync();
+        st_sync();
         if (row < a.d) {
 #pragma unroll
           for (int j = 0; j < EC; j += 4) {
@@ -369,6 +403,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
           }
         }
+        st_sync();
       } else if (row < a.d) {
 #pragma unroll
         for (int j = 0; j < EC; ++j)
@@ -395,83 +430,71 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           *reinterpret_cast<uint4*>(se + SM::E + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-    };
-    auto head_ready = [&](int c) { return c == 0 && g == 0 && a.in_ready; };
-    math_sync();  // the decay tables; the staged state has been read
-    if (init) put_state(fast ? pw[LC - (head_ready(0) ? 1 : 0)] : 1.f);
-    float wk[8];  // weights of this thread's tokens in the transposed keys
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      wk[2 * i] = bw[cg * 32 + i * 8 + 2 * (lane & 3)];
-      wk[2 * i + 1] = bw[cg * 32 + i * 8 + 2 * (lane & 3) + 1];
-    }
-    const uint32_t k_at = (uint32_t)((quad >> 1) * LA_BLOCK + (cg * 32 + (lane & 7)) * 128 +
-                                     ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
-
-    // O of chunk c, whose products have finished, leaves
-    auto put_out = [&](int c) {
-      const int m = tokens(c), r0 = a.reverse ? LC - m : 0;
-      uint8_t* vt = sv + (c & 1) * SM::V;
-#pragma unroll
-      for (int q = 0; q < EC; q += 16) {
-        uint32_t v[16], y[8];
-        tmem_ld16(lanes + TM_O + j0 + q, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          float x0 = __uint_as_float(v[2 * u]), x1 = __uint_as_float(v[2 * u + 1]);
-          mul2(x0, x1, r_out, r_out);
-          y[u] = pack_bf16(x0, x1);
-        }
-        const int j = j0 + q;
-        if (m == LC) {
-          *reinterpret_cast<uint4*>(vt + sw_off(row, j, LC)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(vt + sw_off(row, j + 8, LC)) = make_uint4(y[4], y[5], y[6], y[7]);
-        } else if (row >= r0 && row < r0 + m) {
-          const long long t = (long long)tile_t(c) + row;
-          char* dst = (char*)a.o.p + ((long long)b * a.o.sb + (long long)h * a.o.sh + t * a.o.st + j) * 2;
-          if (j < a.dv) *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-          if (j + 8 < a.dv) *reinterpret_cast<uint4*>(dst + 16) = make_uint4(y[4], y[5], y[6], y[7]);
-        }
-      }
       fence_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->staged[c & 1]);
+      if (lane == 0) mbar_arrive(&bar->est);
     };
+    const bool ready0 = g == 0 && a.in_ready;       // the first chunk's E is decayed already
+    if (!local) {
+      if (init) put_state(fast ? decay_pow(ld, (float)(LC - (ready0 ? 1 : 0))) : 1.f);
+      else if (lane == 0) mbar_arrive(&bar->est);
+    }
 
-    int c = 0;
-    for (; c < chunks; ++c) {
-      const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
+    // weighted keys a^(m-1-s) k_s of chunk c, transposed: 32 state rows x 64 tokens per warp;
+    // the pieces but the high one (all, if two are enough) to TMEM
+    const uint32_t k_at = (uint32_t)((quad >> 1) * LA_BLOCK + (hf * 64 + (lane & 7)) * 128 +
+                                     ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
+    // a chunk of m tokens weights its keys by a^(m-1-s) (descending: by rows from the other end)
+    auto put_weights = [&](int m) {
+      if (mt < LC) {
+        const int e = a.reverse ? mt - (LC - m) : m - 1 - mt;
+        kw[mt] = e < 0 ? 0.f : decay_pow(ld, (float)e);
+      }
+    };
+    put_weights(LC);
+    st_sync();
+    auto put_keys = [&](int c) -> bool {
       const int m = tokens(c);
-      const int r0 = a.reverse ? LC - m : 0;        // the tokens' rows: [r0, r0 + m)
-      if (!la_wait_warp(&bar->full_k[ph], ph2, abort)) break;
-
-      // weighted keys a^(m-1-s) k_s, transposed: 32 state rows x 32 tokens per warp
-      uint32_t khi[2][8];
-      {
-        const uint32_t kt = smem_u32(sk + ph * SM::K) + k_at;
-        uint32_t md[2][8], lo[2][8];
+      if (!la_wait_warp(&bar->full_k[c & 1], (c >> 1) & 1, abort)) return false;
+      uint8_t* kb = sk + (c & 1) * SM::K;
+      if (m < LC) {
+        // (a head has one such chunk, its last.)  Rows behind the sequence's end may hold
+        // anything, NaN included, which a weight of zero does not remove: they are cleared
+        // (before a sequence's start, where descending tiles end, TMA fills zeros)
+        if (!la_wait_warp(&bar->full_v[c & 1], (c >> 1) & 1, abort)) return false;
+        if (!a.reverse) {
+          for (int x = mt; x < (LC - m) * (DK / 8); x += ST)
+            *reinterpret_cast<uint4*>(kb + sw_off(m + x / (DK / 8), (x % (DK / 8)) * 8, LC)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int x = mt; x < (LC - m) * (DV / 8); x += ST)
+            *reinterpret_cast<uint4*>(sv + (c & 1) * SM::V + sw_off(m + x / (DV / 8), (x % (DV / 8)) * 8, LC)) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        // every warp has read the full chunks' weights before any passes the first barrier
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->cleared);
+        if (!la_wait_warp(&bar->cleared, 0, abort)) return false;
+        put_weights(m);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->cleared);
+        if (!la_wait_warp(&bar->cleared, 1, abort)) return false;
+      }
+      const uint32_t kt = smem_u32(kb) + k_at;
+      // rolled: the groups' code has to share the instruction cache
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {                 // 16 tokens
+        uint32_t md[2][4], lo[2][4];
 #pragma unroll
-        for (int sb = 0; sb < 4; ++sb) {
+        for (int sb = 0; sb < 2; ++sb) {
           uint32_t x4[4] = {0u, 0u, 0u, 0u};
-          if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + sb * 1024, x4);
-          float w0 = wk[2 * sb], w1 = wk[2 * sb + 1];
-          if (m < LC) {
-            const int s = cg * 32 + sb * 8 + 2 * (lane & 3);
-            const int e = a.reverse ? s - r0 : m - 1 - s, e1 = a.reverse ? e + 1 : e - 1;
-            const uint32_t keep = (e >= 0 ? 0xffffu : 0u) | (e1 >= 0 ? 0xffff0000u : 0u);  // not NaN times 0
-            w0 = pw[e < 0 ? 0 : e];
-            w1 = pw[e1 < 0 ? 0 : e1];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x4[u] &= keep;
-          }
+          if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + (q * 2 + sb) * 1024, x4);
+          const float2 w = *reinterpret_cast<const float2*>(kw + hf * 64 + (q * 2 + sb) * 8 + 2 * (lane & 3));
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float x0 = __uint_as_float(x4[u] << 16), x1 = __uint_as_float(x4[u] & 0xffff0000u);
-            mul2(x0, x1, w0, w1);
+            mul2(x0, x1, w.x, w.y);
             const int at = sb * 2 + (u & 1);
-            khi[u >> 1][at] = pack_high(x0, x1);
+            md[u >> 1][at] = pack_high(x0, x1);
             below_high(x0, x1);
             if (three) {
               md[u >> 1][at] = pack_high(x0, x1);
@@ -482,144 +505,72 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + cg * 16;
-          tmem_st_16x128_x4(at + TM_K0, lo[u]);
-          if (three) tmem_st_16x128_x4(at + TM_K1, md[u]);
-          else tmem_st_16x128_x4(at + TM_K1, khi[u]);
+          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + hf * 32 + q * 8;
+          tmem_st_16x128_x2(at + TM_K0, lo[u]);
+          tmem_st_16x128_x2(at + TM_K1, md[u]);
         }
-      }
-      if (m < LC && !a.reverse) {
-        // rows behind the sequence's end may hold anything, NaN included, which a weight of
-        // zero does not remove: V's rows are cleared
-        if (!la_wait_warp(&bar->full_v[ph], ph2, abort)) break;
-        for (int x = mt; x < (LC - m) * (DV / 8); x += MT) {
-          const int r = m + x / (DV / 8), cj = (x % (DV / 8)) * 8;
-          *reinterpret_cast<uint4*>(sv + ph * SM::V + sw_off(r, cj, LC)) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_async_smem();
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->kt);
+      return true;
+    };
 
-      if (!local) {
-        if (c > 0) {
-          // E's pieces (the previous chunk's have been read) and the previous chunk's rows of O
-          if (!la_wait_warp(&bar->o1, (c - 1) & 1, abort)) break;
-          put_state(fast ? pw[LC] : 1.f);
-          if (!la_wait_warp(&bar->o2[(c - 1) & 1], ((c - 1) >> 1) & 1, abort)) break;
+    const float a_full = decay_pow(ld, (float)LC);
+    if (chunks > 0 && put_keys(0)) {
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t ph = c & 1;
+        if (three) {
+          // the keys' high piece takes the low one's place once that has been read
+          if (!la_wait_warp(&bar->u1, ph, abort)) break;
           tc_fence_after();
-          put_out(c - 1);
-        } else {
-          fence_async_smem();  // the first pieces
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive(&bar->next);
-      }
-      if (three) {
-        // the keys' high piece takes the low one's place once that has been read
-        if (!la_wait_warp(&bar->u1, ph, abort)) break;
-        tc_fence_after();
+          const uint32_t kt = smem_u32(sk + ph * SM::K) + k_at;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t hi[2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) tmem_st_16x128_x4(lanes + ((uint32_t)(u * 16) << 16) + cg * 16 + TM_K0, khi[u]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->khi);
-      }
-      if (!local) {
-        // P pieces in place, 16 columns (8 of hi, 8 of lo) at a time: thread = token row.
-        // The warp's 32 x 32 block is behind the tokens, ahead of them (zero), or on the diagonal.
-        if (!la_wait_warp(&bar->p, ph, abort)) break;
-        tc_fence_after();
-        const int dq = a.reverse ? cg - quad : quad - cg;
+            for (int sb = 0; sb < 2; ++sb) {
+              uint32_t x4[4] = {0u, 0u, 0u, 0u};
+              if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + (q * 2 + sb) * 1024, x4);
+              const float2 w = *reinterpret_cast<const float2*>(kw + hf * 64 + (q * 2 + sb) * 8 + 2 * (lane & 3));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int s0 = cg * 32 + q * 16;
-          uint32_t pc[16];
-          if (dq < 0) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pc[i] = 0u;
-          } else {
-            uint32_t v[16];
-            tmem_ld16(lanes + TM_P + s0, v);
-            tmem_wait_ld();
-            if (fast) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(bw + s0 + i);
-                float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
-                float x2 = __uint_as_float(v[i + 2]), x3 = __uint_as_float(v[i + 3]);
+              for (int u = 0; u < 4; ++u) {
+                float x0 = __uint_as_float(x4[u] << 16), x1 = __uint_as_float(x4[u] & 0xffff0000u);
                 mul2(x0, x1, w.x, w.y);
-                mul2(x2, x3, w.z, w.w);
-                v[i] = __float_as_uint(x0); v[i + 1] = __float_as_uint(x1);
-                v[i + 2] = __float_as_uint(x2); v[i + 3] = __float_as_uint(x3);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int e = a.reverse ? s0 + i - row : row - s0 - i;
-                v[i] = __float_as_uint(__uint_as_float(v[i]) * pw[e < 0 ? 0 : e]);
+                hi[u >> 1][sb * 2 + (u & 1)] = pack_high(x0, x1);
               }
             }
-            if (dq == 0) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (a.reverse ? q * 16 + i < lane : q * 16 + i > lane) v[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float x0 = __uint_as_float(v[2 * i]), x1 = __uint_as_float(v[2 * i + 1]);
-              pc[i] = pack_high(x0, x1);
-              below_high(x0, x1);
-              pc[8 + i] = pack_bf16(x0, x1);
-            }
+            for (int u = 0; u < 2; ++u)
+              tmem_st_16x128_x2(lanes + ((uint32_t)(u * 16) << 16) + hf * 32 + q * 8 + TM_K0, hi[u]);
           }
-          tmem_st16(lanes + TM_P + s0, pc);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->khi);
         }
-        if (!fast && (init != nullptr || c > 0)) {
-          // O = Q E so far: decay each token's row
-          if (!la_wait_warp(&bar->o1, ph, abort)) break;
-          tc_fence_after();
-          const int u = a.reverse ? LC - 1 - row : row;
-          const float f = pw[u + (head_ready(c) ? 0 : 1)];
+        // E' = a^len E + U
+        if (!la_wait_warp(&bar->u2, ph, abort)) break;
+        tc_fence_after();
+        {
+          const int len = tokens(c) - (c == 0 && ready0 ? 1 : 0);
+          const float f = len == LC ? a_full : decay_pow(ld, (float)len);
+          uint32_t v[EC / 32][32];
 #pragma unroll
-          for (int q = 0; q < EC; q += 16) {
-            uint32_t v[16];
-            tmem_ld16(lanes + TM_O + j0 + q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st16(lanes + TM_O + j0 + q, v);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->mid);
-      }
-
-      // E' = a^len E + U
-      if (!la_wait_warp(&bar->u2, ph, abort)) break;
-      tc_fence_after();
-      {
-        const float f = pw[m - (head_ready(c) ? 1 : 0)];
-#pragma unroll
-        for (int q = 0; q < EC; q += 16) {
-          uint32_t v[16];
-          tmem_ld16(lanes + TM_U + j0 + q, v);
+          for (int q = 0; q < EC / 32; ++q) tmem_ld32(lanes + TM_U + j0 + q * 32, v[q]);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; i += 2)
-            fma2(S[q + i], S[q + i + 1], f, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          for (int j = 0; j < EC; j += 2)
+            fma2(S[j], S[j + 1], f, __uint_as_float(v[j / 32][j % 32]), __uint_as_float(v[j / 32][j % 32 + 1]));
         }
-      }
-    }
-    if (!local && chunks > 0 && c == chunks) {
-      if (la_wait_warp(&bar->o2[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, abort)) {
-        tc_fence_after();
-        put_out(chunks - 1);
+        if (c + 1 < chunks) {
+          if (!put_keys(c + 1)) break;
+          if (!local) {  // E's pieces, once Q E has read the ones before
+            if (!la_wait_warp(&bar->o1, ph, abort)) break;
+            put_state(fast ? a_full : 1.f);
+          }
+        }
       }
     }
     // last state: the segment's slot, or the caller's
@@ -629,13 +580,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const long long osi = local ? a.dv : a.si, osj = local ? 1 : a.sj;
       const float w = local || n == 0 ? 1.f : a.st_scale * (a.out_decay ? decay_pow(ld, 1.f) : 1.f);
       if (osj == 1 && (a.dv & 3) == 0 && ((uintptr_t)dst & 15) == 0 && (osi & 3) == 0) {
-        if (row < a.d) {  // every product that read E's pieces has finished
+        // Q E of the last chunk has to have read E's pieces
+        if (!local && chunks > 0) la_wait_warp(&bar->o1, (chunks - 1) & 1, abort);
+        if (row < a.d) {
 #pragma unroll
           for (int j = 0; j < EC; j += 4)
             *chunk_at(row, (j0 + j) >> 2) = make_float4(S[j] * w, S[j + 1] * w, S[j + 2] * w, S[j + 3] * w);
         }
-        math_sync();
-        for (int x = mt; x < a.d * CH; x += MT) {
+        st_sync();
+        for (int x = mt; x < a.d * CH; x += ST) {
           const int r = x / CH, ch = x - r * CH;
           if (4 * ch < a.dv && !*abort) *reinterpret_cast<float4*>(dst + r * osi + 4 * ch) = *chunk_at(r, ch);
         }
@@ -643,6 +596,139 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
         for (int j = 0; j < EC; ++j)
           if (j0 + j < a.dv) dst[row * osi + (j0 + j) * osj] = S[j] * w;
+      }
+    }
+  } else if (warp >= LA_ROLE_WARPS + LA_ST_WARPS) {
+    // ---------------- scores and output ----------------
+    regs_dec<LA_PO_REGS>();
+    const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS - LA_ST_WARPS) >> 2;
+    const int row = quad * 32 + lane;               // TMEM lane: token row
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int mt = threadIdx.x - (LA_ROLE_WARPS + LA_ST_WARPS) * 32;
+    constexpr int OC = DV / 2;                      // columns of O per thread
+    const int j0 = hf * OC;
+    for (int j = mt; j <= LC; j += LA_PO_WARPS * 32) {
+      pw[j] = decay_pow(ld, (float)j);
+      if (j < LC) bw[j] = decay_pow(ld, (float)(a.reverse ? j : LC - 1 - j));
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(LA_PO_WARPS * 32) : "memory");
+    // what multiplies a finished row of O
+    const float r_out = fast ? a.out_scale * expf(ld * (float)(a.reverse ? -row : row - (LC - 1))) : a.out_scale;
+
+    for (int c = 0; c < chunks && !local; ++c) {
+      const uint32_t ph = c & 1;
+      // P pieces in place, 16 columns (8 of hi, 8 of lo) at a time: a warp's 32 x 32 blocks are
+      // behind the tokens, ahead of them (zero), or on the diagonal
+      if (!la_wait_warp(&bar->p, ph, abort)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int blk = hf * 2; blk < hf * 2 + 2; ++blk) {
+        const int dq = a.reverse ? blk - quad : quad - blk;
+        const int s0 = blk * 32;
+        uint32_t v[32];
+        if (dq < 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        } else {
+          tmem_ld32(lanes + TM_P + s0, v);
+          tmem_wait_ld();
+          if (fast) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(bw + s0 + i);
+              float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
+              float x2 = __uint_as_float(v[i + 2]), x3 = __uint_as_float(v[i + 3]);
+              mul2(x0, x1, w.x, w.y);
+              mul2(x2, x3, w.z, w.w);
+              v[i] = __float_as_uint(x0); v[i + 1] = __float_as_uint(x1);
+              v[i + 2] = __float_as_uint(x2); v[i + 3] = __float_as_uint(x3);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int e = a.reverse ? s0 + i - row : row - s0 - i;
+              v[i] = __float_as_uint(__uint_as_float(v[i]) * pw[e < 0 ? 0 : e]);
+            }
+          }
+          if (dq == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (a.reverse ? i < lane : i > lane) v[i] = 0u;
+          }
+          // 16 columns become 8 of hi pieces and 8 of lo
+#pragma unroll
+          for (int q = 0; q < 32; q += 16) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x0 = __uint_as_float(v[q + 2 * i]), x1 = __uint_as_float(v[q + 2 * i + 1]);
+              hi[i] = pack_high(x0, x1);
+              below_high(x0, x1);
+              lo[i] = pack_bf16(x0, x1);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[q + i] = hi[i];
+              v[q + 8 + i] = lo[i];
+            }
+          }
+        }
+        tmem_st32(lanes + TM_P + s0, v);
+      }
+      if (!fast && (init != nullptr || c > 0)) {
+        // O = Q E so far: decay each token's row
+        if (!la_wait_warp(&bar->o1, ph, abort)) break;
+        tc_fence_after();
+        const int u = a.reverse ? LC - 1 - row : row;
+        const float f = pw[u + (c == 0 && g == 0 && a.in_ready ? 0 : 1)];
+#pragma unroll 1
+        for (int q = 0; q < OC; q += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + TM_O + j0 + q, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+          tmem_st16(lanes + TM_O + j0 + q, v);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->mid);
+
+      // O leaves: through V's stage and TMA, or (partial chunk) straight to its rows
+      if (!la_wait_warp(&bar->o2[ph], (c >> 1) & 1, abort)) break;
+      tc_fence_after();
+      const int m = tokens(c), r0 = a.reverse ? LC - m : 0;
+      uint8_t* vt = sv + ph * SM::V;
+#pragma unroll 1
+      for (int q = 0; q < OC; q += 32) {
+        uint32_t v[32];
+        tmem_ld32(lanes + TM_O + j0 + q, v);
+        tmem_wait_ld();
+        const int j = j0 + q;
+        const long long t = (long long)tile_t(c) + row;
+        char* dst = (char*)a.o.p + ((long long)b * a.o.sb + (long long)h * a.o.sh + t * a.o.st + j) * 2;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x0 = __uint_as_float(v[i + 2 * u]), x1 = __uint_as_float(v[i + 2 * u + 1]);
+            mul2(x0, x1, r_out, r_out);
+            y[u] = pack_bf16(x0, x1);
+          }
+          if (m == LC) *reinterpret_cast<uint4*>(vt + sw_off(row, j + i, LC)) = make_uint4(y[0], y[1], y[2], y[3]);
+          else if (row >= r0 && row < r0 + m && j + i < a.dv)
+            *reinterpret_cast<uint4*>(dst + i * 2) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar->staged[ph]);
+        mbar_arrive(&bar->ofree);
       }
     }
   }
