@@ -13,27 +13,30 @@
 // as a^128 E, and R_t multiplies the finished row of O.  A head whose a^128 is out of range
 // (|log a^128| > LA_RANGE) takes the weights element by element and scales Q E in place.
 //
-// Precision: the inputs are bf16, exact operands.  What is not exact in bf16 enters as pieces:
-// P (weighted) and E as hi + lo (2^-17 left out; O is rounded to bf16 afterwards), the
-// weighted keys of U as hi + mid + lo where the state is handed on in fp32 (exact to fp32),
-// else as two.  U adds the small pieces first, so few of the accumulator's roundings (which
+// Precision: the inputs are bf16, exact operands.  P (weighted) and E enter their product
+// rounded to bf16 once, as O is on its way out: every term of O passes through one of the two,
+// so O is sqrt(2) bf16 roundings off fp32 arithmetic (measured 2.3e-3 of its norm against
+// 1.65e-3; with both as two pieces 1.65e-3, and a chunk 0.6 us longer).  What reaches the state
+// is not rounded: the weighted keys of U as hi + mid + lo where the state is handed on in fp32 (exact to fp32),
+// else as two (2^-17 left out).  U adds the small pieces first, so few of the accumulator's roundings (which
 // truncate) are at full size: the state is 9e-8 off against 6e-7 the other way round.  E is
 // kept in fp32 registers and U is a fresh accumulator per chunk, so the tensor cores' running
 // sums span one chunk only.
 //
 // CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one;
-// the rows of O leave through V's stage), warp 1 owns TMEM and issues the MMAs (one thread),
-// warps 4-11 carry the state, warps 12-19 the scores and the output: a warp reads TMEM lanes
-// 32 (w % 4).. and one half of the columns.  TMEM (512 columns): P fp32, overwritten in place
-// by its two bf16 pieces (operand A of P V); O; U; two pieces of the weighted, transposed keys
-// (operand A of U; the high piece waits in registers and takes the low one's place).
-// Per chunk c, in order:
+// the rows of O leave through shared memory), warp 1 owns TMEM and issues the MMAs (one thread),
+// warps 4-11 weight the keys, 12-19 the scores, 20-27 carry the state and the output: a warp
+// reads TMEM lanes 32 (w % 4).. and one half of the columns.  TMEM (512 columns): P fp32,
+// overwritten in place by its bf16 pairs (operand A of P V); O; U; two pieces of the
+// weighted, transposed keys (operand A of U; the high piece waits in registers and takes the
+// low one's place).  Per chunk c, in order:
 //   MMA     U lo, mid(c)   P(c)   U hi(c)        Q E(c)               P V(c)
-//   state         K hi(c)              E(c), K pieces(c+1), E pieces(c+1)
-//   scores  O out(c-1)                 P pieces(c)
-// so the MMAs of a chunk (8 products of 128^3, 4096 cycles at the dense rate) follow one another
-// while both groups work beside them.  (With all sixteen warps doing everything in turn, a
-// chunk took the sum of the steps' latencies: 5.5 us.)
+//   keys          K hi(c)              K pieces(c+1)
+//   scores                        P bf16(c)
+//   state   O out(c-1)                 E(c)      E bf16(c+1)
+// so the MMAs of a chunk (6 products of 128^3, 3072 cycles at the dense rate) follow one another
+// while the groups work beside them.  (With the groups' steps done in turn by the same warps a
+// chunk took the sum of their latencies, 5.5 us of 148 heads at d = d_v = 128.)
 // Bound: HBM for d = d_v = 128 (128 KB per chunk, 5500 cycles of an SM's share at 6.46 TB/s).
 #include <cstdio>
 
@@ -47,14 +50,14 @@ using namespace sm100;
 namespace {
 
 constexpr int LC = 128;                  // tokens per chunk
-// Warps by warpgroup (register shares go by warpgroups): four of roles (two idle), eight that
-// carry the state (weighted keys, E), eight for the scores and the output.  640 threads launch
-// at 96 registers and redistribute them.
-constexpr int LA_ROLE_WARPS = 4, LA_ST_WARPS = 8, LA_PO_WARPS = 8;
-constexpr int LA_THREADS = (LA_ROLE_WARPS + LA_ST_WARPS + LA_PO_WARPS) * 32;
-constexpr int LA_ROLE_REGS = 48, LA_ST_REGS = 136, LA_PO_REGS = 80;
-static_assert(32 * (LA_ROLE_WARPS * LA_ROLE_REGS + LA_ST_WARPS * LA_ST_REGS + LA_PO_WARPS * LA_PO_REGS) <=
-                  LA_THREADS * 96, "registers");
+// Warps by warpgroups (register shares go by warpgroup): four of roles (two idle), eight for the
+// weighted keys, eight for the scores, eight for the state and the output.  896 threads launch
+// at 72 registers and redistribute them.
+constexpr int LA_ROLE_WARPS = 4, LA_GROUP_WARPS = 8, LA_GROUP = LA_GROUP_WARPS * 32;
+constexpr int LA_THREADS = LA_ROLE_WARPS * 32 + 3 * LA_GROUP;
+constexpr int LA_ROLE_REGS = 56, LA_KEY_REGS = 64, LA_SCORE_REGS = 64, LA_STATE_REGS = 96;
+static_assert(LA_ROLE_WARPS * 32 * LA_ROLE_REGS + LA_GROUP * (LA_KEY_REGS + LA_SCORE_REGS + LA_STATE_REGS) <=
+                  LA_THREADS * 72, "registers");
 constexpr uint64_t LA_TIMEOUT_NS = 200ull * 1000 * 1000;  // any single wait
 constexpr float LA_RANGE = 60.f;         // largest |log a^128| taken through column weights
 constexpr int LA_BLOCK = LC * 128;       // bytes of a 64-column block of 128 rows
@@ -65,14 +68,17 @@ __device__ int g_la_status = DEV_OK;     // latched by a kernel whose wait ran o
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_K1 = 448, TM_COLS = 512;
 
 struct TcBars {
-  uint64_t full_q, full_k[2], full_v[2], free_k[2], staged[2], o2[2];
-  uint64_t p, o1, kt, khi, u1, mid, u2, est, ofree, cleared, drain, stall;
+  uint64_t full_q, full_k[2], full_v[2], free_k[2], o2[2];
+  uint64_t p, o1, staged, kt, khi, u1, mid, u2, est, ofree, ufree, cleared, store, drain, stall;
 };
 
 template <int DK, int DV>
 struct TcSmem {
   static constexpr int Q = LC * DK * 2, K = LC * DK * 2, V = LC * DV * 2, E = DK * DV * 2;
-  static constexpr int off_k = Q, off_v = off_k + 2 * K, off_e = off_v + 2 * V, off_tab = off_e + 2 * E;
+  static constexpr int off_k = Q, off_v = off_k + 2 * K, off_o = off_v + 2 * V, off_e = off_o + V;
+  // states pass through O's rows and E's room (V + E >= DK * DV * 4 for V = 128 rows)
+  static constexpr int off_tab = off_e + E;
+  static_assert(V + E >= DK * DV * 4, "room for a state in fp32");
   static constexpr int need = off_tab + 4 * (3 * LC + 4) + (int)sizeof(TcBars) + 16 + 1024;
   // one CTA per SM: each holds all of TMEM
   static constexpr int bytes = need > 120 * 1024 ? need : 120 * 1024;
@@ -104,8 +110,8 @@ struct Wait {
   uint64_t* bar;
   uint32_t parity;
 };
-__device__ __forceinline__ bool la_wait_each(int lane, volatile int* abort, Wait a, Wait b, Wait c) {
-  const Wait w = lane == 0 ? a : lane == 1 ? b : c;
+__device__ __forceinline__ bool la_wait_each(int lane, volatile int* abort, Wait a, Wait b, Wait c, Wait d) {
+  const Wait w = lane == 0 ? a : lane == 1 ? b : lane == 2 ? c : d;
   return __all_sync(0xffffffffu, la_wait(w.bar, w.parity, abort)) != 0;
 }
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
@@ -123,8 +129,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // rounded 
 __device__ __forceinline__ uint32_t pack_high(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
-__device__ __forceinline__ void below_high(float& x, float& y) {
-  sub2(x, y, __uint_as_float(__float_as_uint(x) & 0xffff0000u), __uint_as_float(__float_as_uint(y) & 0xffff0000u));
+// x, y less the pair of bf16 in p, exact (one mixed-precision operation each).
+__device__ __forceinline__ void below_high(uint32_t p, float& x, float& y) {
+  asm("{\n .reg .b16 l, u, m;\n mov.b32 {l, u}, %2;\n mov.b16 m, 0xBF80;\n fma.rn.f32.bf16 %0, l, m, %0;\n "
+      "fma.rn.f32.bf16 %1, u, m, %1;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "r"(p));
 }
 
 // Byte of element (row, col) in a tile of 64-column blocks of `rows` 128-byte rows, swizzled.
@@ -148,7 +158,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   using SM = TcSmem<DK, DV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sq = smem, *sk = smem + SM::off_k, *sv = smem + SM::off_v, *se = smem + SM::off_e;
+  uint8_t *sq = smem, *sk = smem + SM::off_k, *sv = smem + SM::off_v, *so = smem + SM::off_o, *se = smem + SM::off_e;
   float* bw = (float*)(smem + SM::off_tab);  // [LC] column weights B_s
   float* kw = bw + LC;                       // [LC] weights of the chunk's keys
   float* pw = kw + LC;                       // [LC + 1] a^j
@@ -169,19 +179,21 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       mbar_init(&bar->full_k[i], 1);
       mbar_init(&bar->full_v[i], 1);
       mbar_init(&bar->free_k[i], 1);
-      mbar_init(&bar->staged[i], LA_PO_WARPS);
       mbar_init(&bar->o2[i], 1);
     }
     mbar_init(&bar->p, 1);
     mbar_init(&bar->o1, 1);
-    mbar_init(&bar->kt, LA_ST_WARPS);
-    mbar_init(&bar->khi, LA_ST_WARPS);
+    mbar_init(&bar->kt, LA_GROUP_WARPS);
+    mbar_init(&bar->khi, LA_GROUP_WARPS);
     mbar_init(&bar->u1, 1);
-    mbar_init(&bar->mid, LA_PO_WARPS);
+    mbar_init(&bar->mid, LA_GROUP_WARPS);
     mbar_init(&bar->u2, 1);
-    mbar_init(&bar->est, LA_ST_WARPS);
-    mbar_init(&bar->ofree, LA_PO_WARPS);
-    mbar_init(&bar->cleared, LA_ST_WARPS);
+    mbar_init(&bar->est, LA_GROUP_WARPS);
+    mbar_init(&bar->ofree, LA_GROUP_WARPS);
+    mbar_init(&bar->ufree, LA_GROUP_WARPS);
+    mbar_init(&bar->cleared, LA_GROUP_WARPS);
+    mbar_init(&bar->staged, LA_GROUP_WARPS);
+    mbar_init(&bar->store, 1);
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
     *abort = 0;
@@ -262,14 +274,16 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
         if (!la_wait(&bar->o1, c & 1, abort)) break;
         load_q(c + 1);
-        if (!la_wait(&bar->staged[c & 1], ph, abort)) break;
-        if (tokens(c) == LC) {  // (the rows of a partial chunk are written by the math warps)
+        if (!la_wait(&bar->o2[c & 1], ph, abort)) break;
+        load_v(c + 2);
+        if (!la_wait(&bar->staged, c & 1, abort)) break;
+        if (tokens(c) == LC) {  // (the rows of a partial chunk are written by the state warps)
           for (int x = 0; x < DV; x += 64)
-            tma_store_4d(&mo, sv + (c & 1) * SM::V + (x >> 6) * LA_BLOCK, x, tile_t(c), h * ps.co.h, b * ps.co.b);
+            tma_store_4d(&mo, so + (x >> 6) * LA_BLOCK, x, tile_t(c), h * ps.co.h, b * ps.co.b);
           bulk_commit();
           bulk_wait_read();
         }
-        load_v(c + 2);
+        mbar_arrive(&bar->store);  // O's rows may be overwritten
       }
       bulk_wait_all();
     }
@@ -289,7 +303,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             umma_bf16_ta(tmem + TM_U, tmem + at + kk * 8, vd + kk * 128, id_v, (first && kk == 0) ? 0u : 1u);
         };
         const bool state = init != nullptr || c > 0;
-        ok = la_wait_each(lane, abort, {&bar->kt, ph}, {&bar->full_v[ph], ph2}, {&bar->full_k[ph], ph2});
+        {  // (ufree: the U of the chunk before has been taken up by the state)
+          const Wait kt{&bar->kt, ph};
+          ok = la_wait_each(lane, abort, kt, {&bar->full_v[ph], ph2}, {&bar->full_k[ph], ph2},
+                            c == 0 ? kt : Wait{&bar->ufree, ph ^ 1});
+        }
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -301,7 +319,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (!local) {
           // (o2 of the chunk before: P's columns are free)
           const Wait q{&bar->full_q, ph};
-          ok = la_wait_each(lane, abort, q, c == 0 ? q : Wait{&bar->o2[ph ^ 1], (uint32_t)(((c - 1) >> 1) & 1)}, q);
+          ok = la_wait_each(lane, abort, q, c == 0 ? q : Wait{&bar->o2[ph ^ 1], (uint32_t)(((c - 1) >> 1) & 1)}, q, q);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -313,7 +331,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 umma_bf16(tmem + TM_P, qd + x * (LA_BLOCK >> 4) + kk * 2, kd + x * (LA_BLOCK >> 4) + kk * 2, id_p,
                           (x | kk) != 0 ? 1u : 0u);
             umma_commit(&bar->p);
-            if (!three) umma_commit(&bar->free_k[ph]);
+            umma_commit(&bar->free_k[ph]);
           }
           __syncwarp();
         }
@@ -323,31 +341,26 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           if (elect_one()) {
             u_piece(TM_K0, false);
             umma_commit(&bar->u2);
-            umma_commit(&bar->free_k[ph]);  // (the state warps re-read K for its high piece)
           }
           __syncwarp();
         }
         if (local) {
-          if (!three) {
-            if (elect_one()) umma_commit(&bar->free_k[ph]);
-            __syncwarp();
-          }
+          if (elect_one()) umma_commit(&bar->free_k[ph]);  // K and V
+          __syncwarp();
           continue;
         }
         // E's pieces, and O's columns (the rows of the previous chunk have left)
         const Wait est{&bar->est, ph};
-        ok = la_wait_each(lane, abort, est, c == 0 ? est : Wait{&bar->ofree, ph ^ 1}, est);
+        ok = la_wait_each(lane, abort, est, c == 0 ? est : Wait{&bar->ofree, ph ^ 1}, est, est);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           if (state) {
             const uint64_t qd = sdesc_k_sw128(q0), ed = sdesc_mn_sw128(e0, DK * 128);
-#pragma unroll 1
-            for (int pc = 0; pc < 2; ++pc)
 #pragma unroll 2
-              for (int kk = 0; kk < DK / 16; ++kk)
-                umma_bf16(tmem + TM_O, qd + (kk >> 2) * (LA_BLOCK >> 4) + (kk & 3) * 2,
-                          ed + pc * (SM::E >> 4) + kk * 128, id_v, (pc | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < DK / 16; ++kk)
+              umma_bf16(tmem + TM_O, qd + (kk >> 2) * (LA_BLOCK >> 4) + (kk & 3) * 2, ed + kk * 128, id_v,
+                        kk != 0 ? 1u : 0u);
           }
           umma_commit(&bar->o1);  // also: Q and E's pieces have been read
         }
@@ -356,10 +369,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll 2
-          for (int gq = 0; gq < 8; ++gq) {  // 16 tokens: hi pieces in 8 columns, then lo
-            umma_bf16_ta(tmem + TM_O, tmem + TM_P + gq * 16, vd + gq * 128, id_v, (state || gq != 0) ? 1u : 0u);
-            umma_bf16_ta(tmem + TM_O, tmem + TM_P + gq * 16 + 8, vd + gq * 128, id_v, 1u);
-          }
+          for (int kk = 0; kk < LC / 16; ++kk)  // (P's bf16 columns: the first 16 of every 32)
+            umma_bf16_ta(tmem + TM_O, tmem + TM_P + (kk >> 1) * 32 + (kk & 1) * 8, vd + kk * 128, id_v,
+                         (state || kk != 0) ? 1u : 0u);
           umma_commit(&bar->o2[ph]);
         }
         __syncwarp();
@@ -368,17 +380,188 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       __syncwarp();
       drain_wait(&bar->drain, 0);
     }
-  } else if (warp >= LA_ROLE_WARPS && warp < LA_ROLE_WARPS + LA_ST_WARPS) {
-    // ---------------- the state: weighted keys, E ----------------
-    regs_inc<LA_ST_REGS>();
+  } else if (warp >= LA_ROLE_WARPS && warp < LA_ROLE_WARPS + LA_GROUP_WARPS) {
+    regs_dec<LA_KEY_REGS>();
+    // ---------------- weighted keys a^(m-1-s) k_s, transposed: 32 state rows x 64 tokens a warp
     const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS) >> 2;
-    const int row = quad * 32 + lane;               // TMEM lane: state row
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    constexpr int EC = DV / 2;                      // columns of the state per thread
-    constexpr int ST = LA_ST_WARPS * 32;
-    const int j0 = hf * EC;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + hf * 32;
     const int mt = threadIdx.x - LA_ROLE_WARPS * 32;
-    auto st_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(ST) : "memory"); };
+    const uint32_t k_at = (uint32_t)((quad >> 1) * LA_BLOCK + (hf * 64 + (lane & 7)) * 128 +
+                                     ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
+    // weights of a chunk of m tokens (descending: by rows from the other end)
+    auto put_weights = [&](int m) {
+      if (mt < LC) {
+        const int e = a.reverse ? mt - (LC - m) : m - 1 - mt;
+        kw[mt] = e < 0 ? 0.f : decay_pow(ld, (float)e);
+      }
+    };
+    put_weights(LC);
+    asm volatile("bar.sync 3, %0;" ::"n"(LA_GROUP) : "memory");
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
+      const int m = tokens(c);
+      if (!la_wait_warp(&bar->full_k[ph], ph2, abort)) break;
+      uint8_t* kb = sk + ph * SM::K;
+      if (m < LC) {
+        // (a head has one such chunk, its last.)  Rows behind the sequence's end may hold
+        // anything, NaN included, which a weight of zero does not remove: they are cleared
+        // (before a sequence's start, where descending tiles end, TMA fills zeros)
+        if (!la_wait_warp(&bar->full_v[ph], ph2, abort)) break;
+        if (!a.reverse) {
+          for (int x = mt; x < (LC - m) * (DK / 8); x += LA_GROUP)
+            *reinterpret_cast<uint4*>(kb + sw_off(m + x / (DK / 8), (x % (DK / 8)) * 8, LC)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int x = mt; x < (LC - m) * (DV / 8); x += LA_GROUP)
+            *reinterpret_cast<uint4*>(sv + ph * SM::V + sw_off(m + x / (DV / 8), (x % (DV / 8)) * 8, LC)) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        // every warp has read the full chunks' weights before any passes the first barrier
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->cleared);
+        if (!la_wait_warp(&bar->cleared, 0, abort)) break;
+        put_weights(m);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->cleared);
+        if (!la_wait_warp(&bar->cleared, 1, abort)) break;
+      }
+      // the previous chunk's U has read the pieces
+      if (c > 0 && !la_wait_warp(&bar->u2, ph ^ 1, abort)) break;
+      tc_fence_after();
+      const uint32_t kt = smem_u32(kb) + k_at;
+      uint32_t khi[8][4];                           // [16 tokens, lane half][.]
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {                 // 16 tokens
+        uint32_t md[2][4], lo[2][4];
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb) {
+          uint32_t x4[4] = {0u, 0u, 0u, 0u};
+          if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + (q * 2 + sb) * 1024, x4);
+          const float2 w = *reinterpret_cast<const float2*>(kw + hf * 64 + (q * 2 + sb) * 8 + 2 * (lane & 3));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x0 = __uint_as_float(x4[u] << 16), x1 = __uint_as_float(x4[u] & 0xffff0000u);
+            mul2(x0, x1, w.x, w.y);
+            const int at = sb * 2 + (u & 1);
+            const uint32_t hi = pack_high(x0, x1);
+            khi[q * 2 + (u >> 1)][at] = hi;
+            below_high(hi, x0, x1);
+            md[u >> 1][at] = hi;
+            if (three) {
+              md[u >> 1][at] = pack_high(x0, x1);
+              below_high(md[u >> 1][at], x0, x1);
+            }
+            lo[u >> 1][at] = pack_bf16(x0, x1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + q * 8;
+          tmem_st_16x128_x2(at + TM_K0, lo[u]);
+          tmem_st_16x128_x2(at + TM_K1, md[u]);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->kt);
+      if (three) {
+        // the keys' high piece takes the low one's place once that has been read
+        if (!la_wait_warp(&bar->u1, ph, abort)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          tmem_st_16x128_x2(lanes + ((uint32_t)((i & 1) * 16) << 16) + (i >> 1) * 8 + TM_K0, khi[i]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->khi);
+      }
+    }
+  } else if (warp >= LA_ROLE_WARPS && warp < LA_ROLE_WARPS + 2 * LA_GROUP_WARPS) {
+    // ---------------- scores: P's pieces in place ----------------
+    regs_dec<LA_SCORE_REGS>();
+    const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS - LA_GROUP_WARPS) >> 2;
+    const int row = quad * 32 + lane;               // TMEM lane: token row
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int mt = threadIdx.x - LA_ROLE_WARPS * 32 - LA_GROUP;
+    for (int j = mt; j <= LC; j += LA_GROUP) {
+      pw[j] = decay_pow(ld, (float)j);
+      if (j < LC) bw[j] = fast ? decay_pow(ld, (float)(a.reverse ? j : LC - 1 - j)) : 1.f;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(LA_GROUP) : "memory");
+    for (int c = 0; c < chunks && !local; ++c) {
+      const uint32_t ph = c & 1;
+      if (!la_wait_warp(&bar->p, ph, abort)) break;
+      tc_fence_after();
+      // a warp's two 32 x 32 blocks are behind the tokens, ahead of them (zero), or on the
+      // diagonal; the halves interleave the blocks, so that their work is even
+#pragma unroll 1
+      for (int blk = hf; blk < 4; blk += 2) {       // 32 columns become 16 of bf16 pairs
+        const int dq = a.reverse ? blk - quad : quad - blk, s0 = blk * 32;
+        uint32_t y[16];
+        if (dq < 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = 0u;
+        } else {
+          uint32_t v[32];
+          tmem_ld32(lanes + TM_P + s0, v);
+          tmem_wait_ld();
+          if (!fast) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int e = a.reverse ? s0 + i - row : row - s0 - i;
+              v[i] = __float_as_uint(__uint_as_float(v[i]) * pw[e < 0 ? 0 : e]);
+            }
+          }
+          if (dq == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (a.reverse ? i < lane : i > lane) v[i] = 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 w = *reinterpret_cast<const float4*>(bw + s0 + 4 * i);
+            float x0 = __uint_as_float(v[4 * i]), x1 = __uint_as_float(v[4 * i + 1]);
+            float x2 = __uint_as_float(v[4 * i + 2]), x3 = __uint_as_float(v[4 * i + 3]);
+            mul2(x0, x1, w.x, w.y);
+            mul2(x2, x3, w.z, w.w);
+            y[2 * i] = pack_bf16(x0, x1);
+            y[2 * i + 1] = pack_bf16(x2, x3);
+          }
+        }
+        tmem_st16(lanes + TM_P + s0, y);
+      }
+      if (!fast && (init != nullptr || c > 0)) {
+        // O = Q E so far: decay each token's row
+        if (!la_wait_warp(&bar->o1, ph, abort)) break;
+        tc_fence_after();
+        const int u = a.reverse ? LC - 1 - row : row;
+        const float f = pw[u + (c == 0 && g == 0 && a.in_ready ? 0 : 1)];
+#pragma unroll 1
+        for (int q = hf * (DV / 2); q < (hf + 1) * (DV / 2); q += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + TM_O + q, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+          tmem_st16(lanes + TM_O + q, v);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->mid);
+    }
+  } else if (warp >= LA_ROLE_WARPS + 2 * LA_GROUP_WARPS) {
+    // ---------------- state and output ----------------
+    regs_inc<LA_STATE_REGS>();
+    const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS - 2 * LA_GROUP_WARPS) >> 2;
+    const int row = quad * 32 + lane;               // TMEM lane: state row, or token row of O
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    constexpr int EC = DV / 2;                      // columns of the state and of O per thread
+    const int j0 = hf * EC;
+    const int mt = threadIdx.x - LA_ROLE_WARPS * 32 - 2 * LA_GROUP;
+    auto st_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(LA_GROUP) : "memory"); };
 
     // States in global memory go through the room of E's pieces when their rows are contiguous
     // (fp32 d x DV, 16-byte chunks swizzled by row: a thread's own row directly would touch 32
@@ -387,10 +570,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
     for (int j = 0; j < EC; ++j) S[j] = 0.f;
     constexpr int CH = DV / 4;
-    auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(se + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
+    auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(so + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
     if (init) {
       if (isj == 1 && (a.dv & 3) == 0 && ((uintptr_t)init & 15) == 0 && (isi & 3) == 0) {
-        for (int x = mt; x < a.d * CH; x += ST) {
+        for (int x = mt; x < a.d * CH; x += LA_GROUP) {
           const int r = x / CH, ch = x - r * CH;
           *chunk_at(r, ch) = 4 * ch < a.dv ? *reinterpret_cast<const float4*>(init + r * isi + 4 * ch)
                                            : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -412,22 +595,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
       for (int j = 0; j < EC; ++j) S[j] *= in_scale;
     }
-    auto put_state = [&](float f) {  // f E as two bf16 pieces, the second operand of Q E
+    auto put_state = [&](float f) {  // f E in bf16, the second operand of Q E
       if (row < DK) {
 #pragma unroll
         for (int j = 0; j < EC; j += 8) {
-          uint32_t hi[4], lo[4];
+          uint32_t y[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float x0 = S[j + 2 * u], x1 = S[j + 2 * u + 1];
             mul2(x0, x1, f, f);
-            hi[u] = pack_high(x0, x1);
-            below_high(x0, x1);
-            lo[u] = pack_bf16(x0, x1);
+            y[u] = pack_bf16(x0, x1);
           }
-          const uint32_t o = sw_off(row, j0 + j, DK);
-          *reinterpret_cast<uint4*>(se + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(se + SM::E + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(se + sw_off(row, j0 + j, DK)) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
       fence_async_smem();
@@ -439,138 +618,70 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       if (init) put_state(fast ? decay_pow(ld, (float)(LC - (ready0 ? 1 : 0))) : 1.f);
       else if (lane == 0) mbar_arrive(&bar->est);
     }
-
-    // weighted keys a^(m-1-s) k_s of chunk c, transposed: 32 state rows x 64 tokens per warp;
-    // the pieces but the high one (all, if two are enough) to TMEM
-    const uint32_t k_at = (uint32_t)((quad >> 1) * LA_BLOCK + (hf * 64 + (lane & 7)) * 128 +
-                                     ((((quad & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
-    // a chunk of m tokens weights its keys by a^(m-1-s) (descending: by rows from the other end)
-    auto put_weights = [&](int m) {
-      if (mt < LC) {
-        const int e = a.reverse ? mt - (LC - m) : m - 1 - mt;
-        kw[mt] = e < 0 ? 0.f : decay_pow(ld, (float)e);
-      }
-    };
-    put_weights(LC);
-    st_sync();
-    auto put_keys = [&](int c) -> bool {
-      const int m = tokens(c);
-      if (!la_wait_warp(&bar->full_k[c & 1], (c >> 1) & 1, abort)) return false;
-      uint8_t* kb = sk + (c & 1) * SM::K;
-      if (m < LC) {
-        // (a head has one such chunk, its last.)  Rows behind the sequence's end may hold
-        // anything, NaN included, which a weight of zero does not remove: they are cleared
-        // (before a sequence's start, where descending tiles end, TMA fills zeros)
-        if (!la_wait_warp(&bar->full_v[c & 1], (c >> 1) & 1, abort)) return false;
-        if (!a.reverse) {
-          for (int x = mt; x < (LC - m) * (DK / 8); x += ST)
-            *reinterpret_cast<uint4*>(kb + sw_off(m + x / (DK / 8), (x % (DK / 8)) * 8, LC)) = make_uint4(0u, 0u, 0u, 0u);
-          for (int x = mt; x < (LC - m) * (DV / 8); x += ST)
-            *reinterpret_cast<uint4*>(sv + (c & 1) * SM::V + sw_off(m + x / (DV / 8), (x % (DV / 8)) * 8, LC)) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        // every warp has read the full chunks' weights before any passes the first barrier
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->cleared);
-        if (!la_wait_warp(&bar->cleared, 0, abort)) return false;
-        put_weights(m);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->cleared);
-        if (!la_wait_warp(&bar->cleared, 1, abort)) return false;
-      }
-      const uint32_t kt = smem_u32(kb) + k_at;
-      // rolled: the groups' code has to share the instruction cache
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {                 // 16 tokens
-        uint32_t md[2][4], lo[2][4];
-#pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-          uint32_t x4[4] = {0u, 0u, 0u, 0u};
-          if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + (q * 2 + sb) * 1024, x4);
-          const float2 w = *reinterpret_cast<const float2*>(kw + hf * 64 + (q * 2 + sb) * 8 + 2 * (lane & 3));
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float x0 = __uint_as_float(x4[u] << 16), x1 = __uint_as_float(x4[u] & 0xffff0000u);
-            mul2(x0, x1, w.x, w.y);
-            const int at = sb * 2 + (u & 1);
-            md[u >> 1][at] = pack_high(x0, x1);
-            below_high(x0, x1);
-            if (three) {
-              md[u >> 1][at] = pack_high(x0, x1);
-              below_high(x0, x1);
-            }
-            lo[u >> 1][at] = pack_bf16(x0, x1);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + hf * 32 + q * 8;
-          tmem_st_16x128_x2(at + TM_K0, lo[u]);
-          tmem_st_16x128_x2(at + TM_K1, md[u]);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->kt);
-      return true;
-    };
-
     const float a_full = decay_pow(ld, (float)LC);
-    if (chunks > 0 && put_keys(0)) {
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t ph = c & 1;
-        if (three) {
-          // the keys' high piece takes the low one's place once that has been read
-          if (!la_wait_warp(&bar->u1, ph, abort)) break;
-          tc_fence_after();
-          const uint32_t kt = smem_u32(sk + ph * SM::K) + k_at;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t hi[2][4];
+    // what multiplies a finished row of O
+    const float r_out = fast ? a.out_scale * expf(ld * (float)(a.reverse ? -row : row - (LC - 1))) : a.out_scale;
+
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = c & 1;
+      const int m = tokens(c);
+      // E' = a^len E + U
+      if (!la_wait_warp(&bar->u2, ph, abort)) break;
+      tc_fence_after();
+      {
+        const int len = m - (c == 0 && ready0 ? 1 : 0);
+        const float f = len == LC ? a_full : decay_pow(ld, (float)len);
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb) {
-              uint32_t x4[4] = {0u, 0u, 0u, 0u};
-              if (DK == 128 || quad < 2) ldmatrix_x4_trans(kt + (q * 2 + sb) * 1024, x4);
-              const float2 w = *reinterpret_cast<const float2*>(kw + hf * 64 + (q * 2 + sb) * 8 + 2 * (lane & 3));
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                float x0 = __uint_as_float(x4[u] << 16), x1 = __uint_as_float(x4[u] & 0xffff0000u);
-                mul2(x0, x1, w.x, w.y);
-                hi[u >> 1][sb * 2 + (u & 1)] = pack_high(x0, x1);
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              tmem_st_16x128_x2(lanes + ((uint32_t)(u * 16) << 16) + hf * 32 + q * 8 + TM_K0, hi[u]);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->khi);
-        }
-        // E' = a^len E + U
-        if (!la_wait_warp(&bar->u2, ph, abort)) break;
-        tc_fence_after();
-        {
-          const int len = tokens(c) - (c == 0 && ready0 ? 1 : 0);
-          const float f = len == LC ? a_full : decay_pow(ld, (float)len);
-          uint32_t v[EC / 32][32];
-#pragma unroll
-          for (int q = 0; q < EC / 32; ++q) tmem_ld32(lanes + TM_U + j0 + q * 32, v[q]);
+        for (int q = 0; q < EC; q += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + TM_U + j0 + q, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < EC; j += 2)
-            fma2(S[j], S[j + 1], f, __uint_as_float(v[j / 32][j % 32]), __uint_as_float(v[j / 32][j % 32 + 1]));
+          for (int i = 0; i < 16; i += 2)
+            fma2(S[q + i], S[q + i + 1], f, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
         }
-        if (c + 1 < chunks) {
-          if (!put_keys(c + 1)) break;
-          if (!local) {  // E's pieces, once Q E has read the ones before
-            if (!la_wait_warp(&bar->o1, ph, abort)) break;
-            put_state(fast ? a_full : 1.f);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->ufree);
+      if (local) continue;
+      if (c + 1 < chunks) {  // E's pieces, once Q E has read the ones before
+        if (!la_wait_warp(&bar->o1, ph, abort)) break;
+        put_state(fast ? a_full : 1.f);
+      }
+      // O leaves: through V's stage and TMA, or (partial chunk) straight to its rows
+      if (!la_wait_warp(&bar->o2[ph], (c >> 1) & 1, abort)) break;
+      if (c > 0 && !la_wait_warp(&bar->store, ph ^ 1, abort)) break;  // the rows before have left
+      tc_fence_after();
+      const int r0 = a.reverse ? LC - m : 0;
+#pragma unroll 1
+      for (int q = 0; q < EC; q += 16) {
+        uint32_t v[16];
+        tmem_ld16(lanes + TM_O + j0 + q, v);
+        tmem_wait_ld();
+        const int j = j0 + q;
+        const long long t = (long long)tile_t(c) + row;
+        char* dst = (char*)a.o.p + ((long long)b * a.o.sb + (long long)h * a.o.sh + t * a.o.st + j) * 2;
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+          uint32_t y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x0 = __uint_as_float(v[i + 2 * u]), x1 = __uint_as_float(v[i + 2 * u + 1]);
+            mul2(x0, x1, r_out, r_out);
+            y[u] = pack_bf16(x0, x1);
           }
+          if (m == LC) *reinterpret_cast<uint4*>(so + sw_off(row, j + i, LC)) = make_uint4(y[0], y[1], y[2], y[3]);
+          else if (row >= r0 && row < r0 + m && j + i < a.dv)
+            *reinterpret_cast<uint4*>(dst + i * 2) = make_uint4(y[0], y[1], y[2], y[3]);
         }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar->staged);
+        mbar_arrive(&bar->ofree);
       }
     }
     // last state: the segment's slot, or the caller's
@@ -580,15 +691,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const long long osi = local ? a.dv : a.si, osj = local ? 1 : a.sj;
       const float w = local || n == 0 ? 1.f : a.st_scale * (a.out_decay ? decay_pow(ld, 1.f) : 1.f);
       if (osj == 1 && (a.dv & 3) == 0 && ((uintptr_t)dst & 15) == 0 && (osi & 3) == 0) {
-        // Q E of the last chunk has to have read E's pieces
-        if (!local && chunks > 0) la_wait_warp(&bar->o1, (chunks - 1) & 1, abort);
+        // (the last chunk's O was waited for, so Q E has read E; its rows have to have left)
+        if (!local && chunks > 0) la_wait_warp(&bar->store, (chunks - 1) & 1, abort);
         if (row < a.d) {
 #pragma unroll
           for (int j = 0; j < EC; j += 4)
             *chunk_at(row, (j0 + j) >> 2) = make_float4(S[j] * w, S[j + 1] * w, S[j + 2] * w, S[j + 3] * w);
         }
         st_sync();
-        for (int x = mt; x < a.d * CH; x += ST) {
+        for (int x = mt; x < a.d * CH; x += LA_GROUP) {
           const int r = x / CH, ch = x - r * CH;
           if (4 * ch < a.dv && !*abort) *reinterpret_cast<float4*>(dst + r * osi + 4 * ch) = *chunk_at(r, ch);
         }
@@ -596,139 +707,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
         for (int j = 0; j < EC; ++j)
           if (j0 + j < a.dv) dst[row * osi + (j0 + j) * osj] = S[j] * w;
-      }
-    }
-  } else if (warp >= LA_ROLE_WARPS + LA_ST_WARPS) {
-    // ---------------- scores and output ----------------
-    regs_dec<LA_PO_REGS>();
-    const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS - LA_ST_WARPS) >> 2;
-    const int row = quad * 32 + lane;               // TMEM lane: token row
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int mt = threadIdx.x - (LA_ROLE_WARPS + LA_ST_WARPS) * 32;
-    constexpr int OC = DV / 2;                      // columns of O per thread
-    const int j0 = hf * OC;
-    for (int j = mt; j <= LC; j += LA_PO_WARPS * 32) {
-      pw[j] = decay_pow(ld, (float)j);
-      if (j < LC) bw[j] = decay_pow(ld, (float)(a.reverse ? j : LC - 1 - j));
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(LA_PO_WARPS * 32) : "memory");
-    // what multiplies a finished row of O
-    const float r_out = fast ? a.out_scale * expf(ld * (float)(a.reverse ? -row : row - (LC - 1))) : a.out_scale;
-
-    for (int c = 0; c < chunks && !local; ++c) {
-      const uint32_t ph = c & 1;
-      // P pieces in place, 16 columns (8 of hi, 8 of lo) at a time: a warp's 32 x 32 blocks are
-      // behind the tokens, ahead of them (zero), or on the diagonal
-      if (!la_wait_warp(&bar->p, ph, abort)) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int blk = hf * 2; blk < hf * 2 + 2; ++blk) {
-        const int dq = a.reverse ? blk - quad : quad - blk;
-        const int s0 = blk * 32;
-        uint32_t v[32];
-        if (dq < 0) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        } else {
-          tmem_ld32(lanes + TM_P + s0, v);
-          tmem_wait_ld();
-          if (fast) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(bw + s0 + i);
-              float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
-              float x2 = __uint_as_float(v[i + 2]), x3 = __uint_as_float(v[i + 3]);
-              mul2(x0, x1, w.x, w.y);
-              mul2(x2, x3, w.z, w.w);
-              v[i] = __float_as_uint(x0); v[i + 1] = __float_as_uint(x1);
-              v[i + 2] = __float_as_uint(x2); v[i + 3] = __float_as_uint(x3);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int e = a.reverse ? s0 + i - row : row - s0 - i;
-              v[i] = __float_as_uint(__uint_as_float(v[i]) * pw[e < 0 ? 0 : e]);
-            }
-          }
-          if (dq == 0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (a.reverse ? i < lane : i > lane) v[i] = 0u;
-          }
-          // 16 columns become 8 of hi pieces and 8 of lo
-#pragma unroll
-          for (int q = 0; q < 32; q += 16) {
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float x0 = __uint_as_float(v[q + 2 * i]), x1 = __uint_as_float(v[q + 2 * i + 1]);
-              hi[i] = pack_high(x0, x1);
-              below_high(x0, x1);
-              lo[i] = pack_bf16(x0, x1);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[q + i] = hi[i];
-              v[q + 8 + i] = lo[i];
-            }
-          }
-        }
-        tmem_st32(lanes + TM_P + s0, v);
-      }
-      if (!fast && (init != nullptr || c > 0)) {
-        // O = Q E so far: decay each token's row
-        if (!la_wait_warp(&bar->o1, ph, abort)) break;
-        tc_fence_after();
-        const int u = a.reverse ? LC - 1 - row : row;
-        const float f = pw[u + (c == 0 && g == 0 && a.in_ready ? 0 : 1)];
-#pragma unroll 1
-        for (int q = 0; q < OC; q += 16) {
-          uint32_t v[16];
-          tmem_ld16(lanes + TM_O + j0 + q, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-          tmem_st16(lanes + TM_O + j0 + q, v);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->mid);
-
-      // O leaves: through V's stage and TMA, or (partial chunk) straight to its rows
-      if (!la_wait_warp(&bar->o2[ph], (c >> 1) & 1, abort)) break;
-      tc_fence_after();
-      const int m = tokens(c), r0 = a.reverse ? LC - m : 0;
-      uint8_t* vt = sv + ph * SM::V;
-#pragma unroll 1
-      for (int q = 0; q < OC; q += 32) {
-        uint32_t v[32];
-        tmem_ld32(lanes + TM_O + j0 + q, v);
-        tmem_wait_ld();
-        const int j = j0 + q;
-        const long long t = (long long)tile_t(c) + row;
-        char* dst = (char*)a.o.p + ((long long)b * a.o.sb + (long long)h * a.o.sh + t * a.o.st + j) * 2;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t y[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float x0 = __uint_as_float(v[i + 2 * u]), x1 = __uint_as_float(v[i + 2 * u + 1]);
-            mul2(x0, x1, r_out, r_out);
-            y[u] = pack_bf16(x0, x1);
-          }
-          if (m == LC) *reinterpret_cast<uint4*>(vt + sw_off(row, j + i, LC)) = make_uint4(y[0], y[1], y[2], y[3]);
-          else if (row >= r0 && row < r0 + m && j + i < a.dv)
-            *reinterpret_cast<uint4*>(dst + i * 2) = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bar->staged[ph]);
-        mbar_arrive(&bar->ofree);
       }
     }
   }
