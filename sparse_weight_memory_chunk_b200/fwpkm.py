@@ -281,106 +281,113 @@ def addressing_metrics(idx, N: int, window: int = 32768, workspace=None, stream=
 
 # ---- operators around the memory -------------------------------------------------------
 # Torch tensors in, torch tensors out; every call only enqueues on `stream` (default: the
-# current stream of the tensors' device).
+# current stream of the tensors' device).  Single tokens and small batches take about as long
+# on the host as on the GPU, so the checks below stay with what costs little.
 
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
+_DTYPES = None
+
+
 def _dtype(t, what):
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    _need(t.dtype == torch.bfloat16, f"{what} must be float32 or bfloat16, not {t.dtype}")
-    return BF16
-
-
-class _on:
-    """The stream handle of a call on `dev`, with `dev` current while the call is made."""
-
-    def __init__(self, dev, stream):
+    global _DTYPES
+    if _DTYPES is None:
         import torch
-        _need(dev.type == "cuda", "the tensors must be on a CUDA device")
-        self.cur = torch.cuda.current_device()
-        self.dev = self.cur if dev.index is None else dev.index
-        if stream is None:
-            stream = torch.cuda.current_stream(self.dev)
-        _need(stream.device_index == self.dev, "the stream is another device's than the tensors")
-        self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        if self.dev != self.cur:
-            import torch
-            torch.cuda.set_device(self.dev)
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.dev != self.cur:
-            import torch
-            torch.cuda.set_device(self.cur)
+        _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be float32 or bfloat16, not {t.dtype}")
+    return code
 
 
-def _side(t, dev, dtype, shape, what):
-    """A contiguous tensor of this type, shape and device (None passes)."""
-    if t is not None:
-        _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == dev and t.is_contiguous(),
-              f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
-    return None if t is None else t.data_ptr()
-
-
-def _scratch(workspace, nbytes, dev, what):
+def _call(t, stream, where, fn, *args):
+    """fn(*args, stream) with the device of `t` current; a non-OK status raises."""
     import torch
+    _need(t.is_cuda, "the tensors must be on a CUDA device")
+    dev = t.get_device()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        _need(stream.device_index == dev, "the stream is another device's than the tensors")
+        handle = stream.cuda_stream
+    cur = torch.cuda.current_device()
+    if cur == dev:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != OK:
+        raise FwpkmError(status, where)
+
+
+def _side(t, like, dtype, shape, what):
+    """The pointer of a contiguous tensor of this type, shape and `like`'s device (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    return t.data_ptr()
+
+
+def _scratch(workspace, nbytes, like, what):
+    """(tensor, pointer, bytes) of a workspace: the caller's, or a new one of nbytes."""
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    _need(workspace.device == dev and workspace.is_contiguous(), f"{what}: the workspace must be contiguous, on {dev}")
-    return workspace
+        if not nbytes:
+            return None, None, 0
+        import torch
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), nbytes
+    _need(workspace.device == like.device and workspace.is_contiguous(),
+          f"{what}: the workspace must be contiguous, on {like.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _scratch_args(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _bytes(fn, where, *args):
+    out = ctypes.c_size_t(0)
+    status = fn(*args, ctypes.byref(out))
+    if status != OK:
+        raise FwpkmError(status, where)
+    return out.value
 
 
 def _lookup_config(table, idx, w, scale):
     import torch
     _need(table.dim() == 2 and (table.stride(1) == 1 or table.shape[1] <= 1),
           "table must be [rows][width], its rows contiguous")
-    _need(idx.dtype in (torch.int32, torch.int64), "idx must be int32 or int64")
+    i64 = idx.dtype == torch.int64
+    _need(i64 or idx.dtype == torch.int32, "idx must be int32 or int64")
     _need(idx.device == table.device and idx.is_contiguous(), "idx must be contiguous, on the table's device")
-    R = 1
+    rows, width = table.shape
+    R, lead = 1, idx.shape
     if w is not None:
         _need(idx.dim() >= 1, "with w the last axis of idx is the bag")
-        R = idx.shape[-1]
-        _side(w, table.device, torch.float32, idx.shape, "w")
-    lead = tuple(idx.shape[:-1]) if w is not None else tuple(idx.shape)
+        R, lead = idx.shape[-1], idx.shape[:-1]
+        _side(w, table, torch.float32, idx.shape, "w")
     n = idx.numel() // R if R else 0
-    cfg = LookupConfig(table.shape[0], max(table.stride(0), table.shape[1]), table.shape[1], table.shape[1], R,
-                       _dtype(table, "table"), I64 if idx.dtype == torch.int64 else I32, scale)
-    return cfg, lead, n
+    return LookupConfig(rows, max(table.stride(0), width), width, width, R, _dtype(table, "table"),
+                        I64 if i64 else I32, scale), lead + (width,), n
 
 
 def lookup(table, idx, w=None, scale=1.0, out=None, stream=None):
     """fwpkm_lookup: scale * table[idx], shape idx.shape + [width]; with weights w (fp32, the
     shape of idx) the last axis of idx is summed: scale * sum_r w[.., r] table[idx[.., r]].
     Indices outside the table read zeros."""
-    import torch
-    cfg, lead, n = _lookup_config(table, idx, w, scale)
-    shape = lead + (table.shape[1],)
+    cfg, shape, n = _lookup_config(table, idx, w, scale)
     if out is None:
-        out = torch.empty(shape, dtype=table.dtype, device=table.device)
-    _side(out, table.device, table.dtype, shape, "out")
-    with _on(table.device, stream) as s:
-        _check(lib().fwpkm_lookup(ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
-                                  None if w is None else w.data_ptr(), n, out.data_ptr(), s), "lookup")
+        out = table.new_empty(shape)
+    else:
+        _side(out, table, table.dtype, shape, "out")
+    _call(table, stream, "lookup", lib().fwpkm_lookup, ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
+          None if w is None else w.data_ptr(), n, out.data_ptr())
     return out
 
 
 def lookup_backward_workspace_size(table, idx, w=None) -> int:
     cfg, _, n = _lookup_config(table, idx, w, 1.0)
-    out = ctypes.c_size_t(0)
-    _check(lib().fwpkm_lookup_backward_workspace_size(ctypes.byref(cfg), n, ctypes.byref(out)),
-           "lookup_backward_workspace_size")
-    return out.value
+    return _bytes(lib().fwpkm_lookup_backward_workspace_size, "lookup_backward_workspace_size", ctypes.byref(cfg), n)
 
 
 def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumulate=False, grad_dtype=None, dw=None,
@@ -390,32 +397,30 @@ def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumula
     accumulate added to the rows that were read (then it must be given); dw (fp32, the shape
     of idx) is None without w or with need_dw=False."""
     import torch
-    cfg, lead, n = _lookup_config(table, idx, w, scale)
-    dev = table.device
-    _side(d_out, dev, table.dtype, lead + (table.shape[1],), "d_out")
+    cfg, shape, n = _lookup_config(table, idx, w, scale)
+    p_out = _side(d_out, table, table.dtype, shape, "d_out")
+    _need(d_out is not None, "d_out is needed")
     _need(not accumulate or d_table is not None, "accumulate needs the d_table to add to")
     if d_table is None:
-        d_table = torch.empty(table.shape, dtype=grad_dtype or table.dtype, device=dev)
-    _need(d_table.shape == table.shape and d_table.device == dev and (d_table.stride(1) == 1 or table.shape[1] <= 1)
+        d_table = torch.empty(table.shape, dtype=grad_dtype or table.dtype, device=table.device)
+    _need(d_table.shape == table.shape and d_table.device == table.device
+          and (d_table.stride(1) == 1 or table.shape[1] <= 1)
           and (table.shape[0] <= 1 or d_table.stride(0) >= table.shape[1]),
           "d_table must have the table's shape and device, its rows contiguous and apart")
     _need(grad_dtype is None or d_table.dtype == grad_dtype, "d_table is not of grad_dtype")
     if w is None or not need_dw:
         _need(dw is None, "dw needs w and need_dw")
+    elif dw is None:
+        dw = torch.empty(idx.shape, dtype=torch.float32, device=table.device)
     else:
-        if dw is None:
-            dw = torch.empty(idx.shape, dtype=torch.float32, device=dev)
-        _side(dw, dev, torch.float32, idx.shape, "dw")
-    nb = ctypes.c_size_t(0)
-    _check(lib().fwpkm_lookup_backward_workspace_size(ctypes.byref(cfg), n, ctypes.byref(nb)), "lookup_backward")
-    ws = _scratch(workspace, nb.value, dev, "lookup_backward")
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_lookup_backward(ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
-                                           None if w is None else w.data_ptr(), d_out.data_ptr(), n,
-                                           d_table.data_ptr(), max(d_table.stride(0), table.shape[1]),
-                                           _dtype(d_table, "d_table"), int(accumulate),
-                                           None if dw is None else dw.data_ptr(), *_scratch_args(ws), s),
-               "lookup_backward")
+        _side(dw, table, torch.float32, idx.shape, "dw")
+    L, c = lib(), ctypes.byref(cfg)
+    keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
+                            _bytes(L.fwpkm_lookup_backward_workspace_size, "lookup_backward", c, n), table,
+                            "lookup_backward")
+    _call(table, stream, "lookup_backward", L.fwpkm_lookup_backward, c, table.data_ptr(), idx.data_ptr(),
+          None if w is None else w.data_ptr(), p_out, n, d_table.data_ptr(), max(d_table.stride(0), table.shape[1]),
+          _dtype(d_table, "d_table"), int(accumulate), None if dw is None else dw.data_ptr(), pw, nw)
     return d_table, dw
 
 
@@ -427,17 +432,18 @@ class BalanceLoss:
 
 def _balance_config(x, idx, mask, kind, coef):
     import torch
-    _need(x.dim() == 3 and (x.stride(2) == 1 or x.shape[2] <= 1), "x must be [groups][tokens][experts], its rows contiguous")
+    _need(x.dim() == 3 and (x.stride(2) == 1 or x.shape[2] <= 1),
+          "x must be [groups][tokens][experts], its rows contiguous")
     _need(kind in BALANCE_KIND, f"kind must be one of {sorted(BALANCE_KIND)}")
     G, T, E = x.shape
     k = 0
     if idx is not None:
         _need(idx.dim() == 3, "idx must be [groups][tokens][k]")
         k = idx.shape[2]
-        _side(idx, x.device, torch.int32, (G, T, k), "idx")
+        _side(idx, x, torch.int32, (G, T, k), "idx")
     if mask is not None:
         _need(mask.dtype in (torch.bool, torch.uint8), "mask must be bool or uint8")
-        _side(mask, x.device, mask.dtype, (G, T), "mask")
+        _side(mask, x, mask.dtype, (G, T), "mask")
     return BalanceConfig(T, max(x.stride(1), E), x.stride(0) if G > 1 else 0, G, E, k, _dtype(x, "x"),
                          BALANCE_KIND[kind], coef)
 
@@ -448,20 +454,19 @@ def balance_loss(x, idx=None, mask=None, kind="load", coef=1.0, workspace=None, 
     [groups][tokens] of the tokens that count."""
     import torch
     cfg = _balance_config(x, idx, mask, kind, coef)
-    dev, G, E = x.device, cfg.groups, cfg.experts
-    nb = ctypes.c_size_t(0)
-    _check(lib().fwpkm_balance_workspace_size(ctypes.byref(cfg), ctypes.byref(nb)), "balance_loss")
-    ws = _scratch(workspace, nb.value, dev, "balance_loss")
+    G, E = cfg.groups, cfg.experts
+    L, c = lib(), ctypes.byref(cfg)
+    keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
+                            _bytes(L.fwpkm_balance_workspace_size, "balance_loss", c), x, "balance_loss")
     r = BalanceLoss()
     r.kind, r.coef = kind, coef
-    f = torch.empty(2 * G * E + G, dtype=torch.float32, device=dev)
+    f = torch.empty(2 * G * E + G, dtype=torch.float32, device=x.device)
     r.usage, r.slope, r.loss = f[:G * E].view(G, E), f[G * E:2 * G * E].view(G, E), f[2 * G * E:]
-    r.counts = None if idx is None else torch.empty(G, E, dtype=torch.int32, device=dev)
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_balance_loss(ctypes.byref(cfg), x.data_ptr(), None if idx is None else idx.data_ptr(),
-                                        None if mask is None else mask.data_ptr(), *_scratch_args(ws),
-                                        r.loss.data_ptr(), None if idx is None else r.counts.data_ptr(),
-                                        r.usage.data_ptr(), r.slope.data_ptr(), s), "balance_loss")
+    r.counts = None if idx is None else torch.empty(G, E, dtype=torch.int32, device=x.device)
+    p = f.data_ptr()
+    _call(x, stream, "balance_loss", L.fwpkm_balance_loss, c, x.data_ptr(), None if idx is None else idx.data_ptr(),
+          None if mask is None else mask.data_ptr(), pw, nw, p + 8 * G * E, None if idx is None else r.counts.data_ptr(),
+          p, p + 4 * G * E)
     return r
 
 
@@ -470,56 +475,50 @@ def balance_loss_backward(x, result: BalanceLoss, mask=None, d_loss=None, dx=Non
     the same x and mask, from d_loss [groups] (None: ones)."""
     import torch
     cfg = _balance_config(x, None, mask, result.kind, result.coef)
-    dev, G, T, E = x.device, *x.shape
-    _side(result.slope, dev, torch.float32, (G, E), "result.slope")
-    _side(d_loss, dev, torch.float32, (G,), "d_loss")
+    G, T, E = x.shape
+    ps = _side(result.slope, x, torch.float32, (G, E), "result.slope")
+    pl = _side(d_loss, x, torch.float32, (G,), "d_loss")
     if dx is None:
-        dx = torch.empty(G, T, E, dtype=x.dtype, device=dev)
-    _side(dx, dev, x.dtype, (G, T, E), "dx")
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_balance_loss_backward(ctypes.byref(cfg), x.data_ptr(),
-                                                 None if mask is None else mask.data_ptr(),
-                                                 result.slope.data_ptr(),
-                                                 None if d_loss is None else d_loss.data_ptr(), dx.data_ptr(), s),
-               "balance_loss_backward")
+        dx = torch.empty(G, T, E, dtype=x.dtype, device=x.device)
+    else:
+        _side(dx, x, x.dtype, (G, T, E), "dx")
+    _call(x, stream, "balance_loss_backward", lib().fwpkm_balance_loss_backward, ctypes.byref(cfg), x.data_ptr(),
+          None if mask is None else mask.data_ptr(), ps, pl, dx.data_ptr())
     return dx
 
 
-def _heads(t, dev, dtype, B, H, T, w, what):
+def _heads(t, like, shape, what):
     """A [B][H][T][w] tensor of any strides with contiguous rows."""
-    _need(t.dim() == 4 and tuple(t.shape) == (B, H, T, w) and t.dtype == dtype and t.device == dev,
-          f"{what} must be a {dtype} tensor of shape {(B, H, T, w)} on {dev}")
+    if t.shape != shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what} must be a {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
     sb, sh, st, se = t.stride()
-    _need(se == 1 or w == 1, f"{what}: the rows must be contiguous")
-    return Heads(t.data_ptr(), sb, sh, st)
+    if se != 1 and shape[3] > 1:
+        raise ValueError(f"{what}: the rows must be contiguous")
+    return ctypes.byref(Heads(t.data_ptr(), sb, sh, st))
 
 
 def _linattn_args(q, k, v, log_decay, scale, lens):
     import torch
     _need(q.dim() == 4 and v.dim() == 4, "q, k, v must be [B][H][T][width]")
-    B, H, T, d = q.shape
-    dv, dev, dt = v.shape[3], q.device, q.dtype
-    hq = _heads(q, dev, dt, B, H, T, d, "q")
-    hk = _heads(k, dev, dt, B, H, T, d, "k")
-    hv = _heads(v, dev, dt, B, H, T, dv, "v")
-    ld = _side(log_decay, dev, torch.float32, (H,), "log_decay")
-    _need(ld is not None, "log_decay is needed")
-    ln = _side(lens, dev, torch.int32, (B,), "lens")
-    return LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale), hq, hk, hv, ld, ln, T
+    qs = q.shape
+    B, H, T, d = qs
+    dv = v.shape[3]
+    hq, hk, hv = _heads(q, q, qs, "q"), _heads(k, q, qs, "k"), _heads(v, q, (B, H, T, dv), "v")
+    _need(log_decay is not None, "log_decay is needed")
+    ld = _side(log_decay, q, torch.float32, (H,), "log_decay")
+    ln = _side(lens, q, torch.int32, (B,), "lens")
+    return ctypes.byref(LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale)), hq, hk, hv, ld, ln, B, H, T, d, dv
 
 
 def _rows_like(t, B, H, T, w):
     """A new [B][H][T][w] tensor in the memory order [B][T][H][w] of a projection's output."""
-    import torch
-    return torch.empty(B, T, H, w, dtype=t.dtype, device=t.device).transpose(1, 2)
+    return t.new_empty((B, T, H, w)).transpose(1, 2)
 
 
 def linear_attention_workspace_size(q, v, backward=False) -> int:
     cfg = LinattnConfig(q.shape[0], q.shape[1], q.shape[3], v.shape[3], _dtype(q, "q"), 1.0)
-    out = ctypes.c_size_t(0)
-    _check(lib().fwpkm_linear_attention_workspace_size(ctypes.byref(cfg), q.shape[2], int(backward),
-                                                       ctypes.byref(out)), "linear_attention_workspace_size")
-    return out.value
+    return _bytes(lib().fwpkm_linear_attention_workspace_size, "linear_attention_workspace_size", ctypes.byref(cfg),
+                  q.shape[2], int(backward))
 
 
 def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, sT=None, final_state=False,
@@ -529,22 +528,19 @@ def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, 
     [B] int32.  sT is None unless given or asked for with final_state.  Rows of o behind a
     sequence's end are left as they were (a new o holds anything there)."""
     import torch
-    cfg, hq, hk, hv, ld, ln, T = _linattn_args(q, k, v, log_decay, scale, lens)
-    dev, B, H, d, dv = q.device, cfg.B, cfg.H, cfg.d, cfg.d_v
+    c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
         o = _rows_like(v, B, H, T, dv)
-    ho = _heads(o, dev, q.dtype, B, H, T, dv, "o")
+    ho = _heads(o, q, (B, H, T, dv), "o")
     if sT is None and final_state:
-        sT = torch.empty(B, H, d, dv, dtype=torch.float32, device=dev)
-    p0 = _side(s0, dev, torch.float32, (B, H, d, dv), "s0")
-    pT = _side(sT, dev, torch.float32, (B, H, d, dv), "sT")
-    nb = ctypes.c_size_t(0)
-    _check(lib().fwpkm_linear_attention_workspace_size(ctypes.byref(cfg), T, 0, ctypes.byref(nb)), "linear_attention")
-    ws = _scratch(workspace, nb.value, dev, "linear_attention")
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_linear_attention(ctypes.byref(cfg), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv), T,
-                                            ld, ln, p0, ctypes.byref(ho), pT, *_scratch_args(ws), s),
-               "linear_attention")
+        sT = torch.empty(B, H, d, dv, dtype=torch.float32, device=q.device)
+    p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
+    pT = _side(sT, q, torch.float32, (B, H, d, dv), "sT")
+    L = lib()
+    keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
+                            _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention", c, T, 0), q,
+                            "linear_attention")
+    _call(q, stream, "linear_attention", L.fwpkm_linear_attention, c, hq, hk, hv, T, ld, ln, p0, ho, pT, pw, nw)
     return o, sT
 
 
@@ -554,26 +550,22 @@ def linear_attention_backward(q, k, v, log_decay, d_o, scale=1.0, s0=None, d_sT=
     final state's gradient d_sT (None: zero).  `grads`: (dq, dk, dv) to fill; ds0 is None with
     state_grad=False.  Rows behind a sequence's end are left as they were."""
     import torch
-    cfg, hq, hk, hv, ld, ln, T = _linattn_args(q, k, v, log_decay, scale, lens)
-    dev, dt, B, H, d, dv = q.device, q.dtype, cfg.B, cfg.H, cfg.d, cfg.d_v
-    ho = _heads(d_o, dev, dt, B, H, T, dv, "d_o")
+    c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
+    ho = _heads(d_o, q, (B, H, T, dv), "d_o")
     if grads is None:
         grads = (_rows_like(q, B, H, T, d), _rows_like(q, B, H, T, d), _rows_like(v, B, H, T, dv))
-    hg = [_heads(t, dev, dt, B, H, T, w, n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
+    hg = [_heads(t, q, (B, H, T, w), n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
     if ds0 is None and state_grad:
-        ds0 = torch.empty(B, H, d, dv, dtype=torch.float32, device=dev)
-    p0 = _side(s0, dev, torch.float32, (B, H, d, dv), "s0")
-    pT = _side(d_sT, dev, torch.float32, (B, H, d, dv), "d_sT")
-    pd = _side(ds0, dev, torch.float32, (B, H, d, dv), "ds0")
-    nb = ctypes.c_size_t(0)
-    _check(lib().fwpkm_linear_attention_workspace_size(ctypes.byref(cfg), T, 1, ctypes.byref(nb)),
-           "linear_attention_backward")
-    ws = _scratch(workspace, nb.value, dev, "linear_attention_backward")
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_linear_attention_backward(ctypes.byref(cfg), ctypes.byref(hq), ctypes.byref(hk),
-                                                     ctypes.byref(hv), T, ld, ln, p0, ctypes.byref(ho), pT,
-                                                     ctypes.byref(hg[0]), ctypes.byref(hg[1]), ctypes.byref(hg[2]), pd,
-                                                     *_scratch_args(ws), s), "linear_attention_backward")
+        ds0 = torch.empty(B, H, d, dv, dtype=torch.float32, device=q.device)
+    p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
+    pT = _side(d_sT, q, torch.float32, (B, H, d, dv), "d_sT")
+    pd = _side(ds0, q, torch.float32, (B, H, d, dv), "ds0")
+    L = lib()
+    keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
+                            _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention_backward", c, T, 1), q,
+                            "linear_attention_backward")
+    _call(q, stream, "linear_attention_backward", L.fwpkm_linear_attention_backward, c, hq, hk, hv, T, ld, ln, p0, ho,
+          pT, *hg, pd, pw, nw)
     return (*grads, ds0)
 
 
@@ -583,19 +575,16 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
     states [B][H][d][d_v], which are updated in place unless state_out is given or
     in_place=False (then a new tensor is)."""
     import torch
-    cfg, hq, hk, hv, ld, ln, T = _linattn_args(q, k, v, log_decay, scale, lens)
-    dev, B, H, d, dv = q.device, cfg.B, cfg.H, cfg.d, cfg.d_v
+    c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
         o = _rows_like(v, B, H, T, dv)
-    ho = _heads(o, dev, q.dtype, B, H, T, dv, "o")
+    ho = _heads(o, q, (B, H, T, dv), "o")
+    _need(state is not None, "state is needed")
+    ps = _side(state, q, torch.float32, (B, H, d, dv), "state")
     if state_out is None:
         state_out = state if in_place else torch.empty_like(state)
-    ps = _side(state, dev, torch.float32, (B, H, d, dv), "state")
-    po = _side(state_out, dev, torch.float32, (B, H, d, dv), "state_out")
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_linear_attention_step(ctypes.byref(cfg), ctypes.byref(hq), ctypes.byref(hk),
-                                                 ctypes.byref(hv), T, ld, ln, ps, ctypes.byref(ho), po, s),
-               "linear_attention_step")
+    po = _side(state_out, q, torch.float32, (B, H, d, dv), "state_out")
+    _call(q, stream, "linear_attention_step", lib().fwpkm_linear_attention_step, c, hq, hk, hv, T, ld, ln, ps, ho, po)
     return o, state_out
 
 
@@ -603,9 +592,9 @@ def linear_attention_sync(device=None, stream=None):
     """fwpkm_linear_attention_sync: wait for the stream and raise what linear-attention kernels
     on the device have latched (a wait that timed out)."""
     import torch
-    dev = torch.device("cuda") if device is None else torch.device(device)
-    with _on(dev, stream) as s:
-        _check(lib().fwpkm_linear_attention_sync(s), "linear_attention_sync")
+    with torch.cuda.device(device):
+        handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+        _check(lib().fwpkm_linear_attention_sync(handle), "linear_attention_sync")
 
 
 class State:
