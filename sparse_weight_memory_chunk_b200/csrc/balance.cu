@@ -25,7 +25,7 @@
 namespace fwpkm {
 namespace {
 
-constexpr int BL_THREADS = 512;
+constexpr int BL_THREADS = 256;
 constexpr int BL_MAX_E = 4096;
 constexpr int BL_JOIN = 1024;
 
@@ -51,21 +51,26 @@ __device__ __forceinline__ void bal_put(float& d, float x) { d = x; }
 __device__ __forceinline__ void bal_put(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
 // A row of E logits over a team of L lanes (L <= 32: lanes of a warp; L = BL_THREADS: the
-// CTA): thread `l` holds elements (j L + l) VEC .. +VEC-1, j < NCH; -inf past E.
+// CTA): thread `l` holds elements (j L + l) VEC .. +VEC-1, j < NCH; -inf past E.  fetch_row
+// issues the loads of row t (false: behind `end`, or masked: nothing is read).
 template <typename T, int VEC, int NCH, int L>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l, float (&v)[VEC * NCH]) {
+__device__ __forceinline__ bool fetch_row(const T* __restrict__ x, const uint8_t* __restrict__ mask, long long t,
+                                          long long end, long long ld, int E, int l, BPack<T, VEC> (&p)[NCH]) {
+  if (t >= end || (mask && !mask[t])) return false;
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     const int e = (j * L + l) * VEC;
-    if (e < E) {
-      const BPack<T, VEC> p = *reinterpret_cast<const BPack<T, VEC>*>(row + e);
-#pragma unroll
-      for (int u = 0; u < VEC; ++u) v[j * VEC + u] = bal_f(p.v[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < VEC; ++u) v[j * VEC + u] = -INFINITY;
-    }
+    if (e < E) p[j] = *reinterpret_cast<const BPack<T, VEC>*>(x + t * ld + e);
   }
+  return true;
+}
+template <typename T, int VEC, int NCH, int L>
+__device__ __forceinline__ void take_row(const BPack<T, VEC> (&p)[NCH], bool on, int E, int l,
+                                         float (&v)[VEC * NCH]) {
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int u = 0; u < VEC; ++u) v[j * VEC + u] = on && (j * L + l) * VEC < E ? bal_f(p[j].v[u]) : -INFINITY;
 }
 
 template <int L, bool MAX>
@@ -135,17 +140,14 @@ balance_sum_kernel(BalArgs a) {
   for (int i = 0; i < NV; ++i) acc[i] = 0.f;
   int n = 0;
   __syncthreads();
-  // every team of a warp takes part in the warp's shuffles, so the loop's trip count is the CTA's
+  // every team of a warp takes part in the warp's shuffles, so the loop's trip count is the CTA's;
+  // a team's next row is on its way while it works on this one
+  BPack<T, VEC> next[NCH];
+  bool next_on = fetch_row<T, VEC, NCH, L>(x, mask, t0 + team, t1, a.ld, a.E, l, next);
   for (long long tb = t0; tb < t1; tb += TEAMS) {
-    const long long t = tb + team;
-    const bool on = t < t1 && (!mask || mask[t]);
     float v[NV];
-    if (on) {
-      load_row<T, VEC, NCH, L>(x + t * a.ld, a.E, l, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = -INFINITY;
-    }
+    take_row<T, VEC, NCH, L>(next, next_on, a.E, l, v);
+    next_on = fetch_row<T, VEC, NCH, L>(x, mask, tb + TEAMS + team, t1, a.ld, a.E, l, next);
     if (team_softmax<NV, L>(v, red)) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] += v[i];
@@ -181,9 +183,11 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
-  double s = 0.0;
-  for (int w = 0; w < BL_JOIN / 32; ++w) s += red[w];
-  return s;
+  static_assert(BL_JOIN == 1024, "one value per lane");
+  x = red[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
 // One CTA per group: the CTAs' partial sums in CTA order -> usage, counts, loss, slope.
@@ -302,16 +306,14 @@ balance_grad_kernel(BalArgs a, const float* __restrict__ slope, const float* __r
     }
   const float gl = d_loss ? d_loss[g] : 1.f;
   const long long step = (long long)gridDim.x * TEAMS;
+  BPack<T, VEC> next[NCH];
+  bool next_on = fetch_row<T, VEC, NCH, L>(x, mask, (long long)blockIdx.x * TEAMS + team, a.T, a.ld, a.E, l, next);
   for (long long tb = (long long)blockIdx.x * TEAMS; tb < a.T; tb += step) {
     const long long t = tb + team;
-    const bool in = t < a.T, on = in && (!mask || mask[t]);
+    const bool in = t < a.T;
     float v[NV];
-    if (on) {
-      load_row<T, VEC, NCH, L>(x + t * a.ld, a.E, l, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = -INFINITY;
-    }
+    take_row<T, VEC, NCH, L>(next, next_on, a.E, l, v);
+    next_on = fetch_row<T, VEC, NCH, L>(x, mask, t + step, a.T, a.ld, a.E, l, next);
     const bool live = team_softmax<NV, L>(v, red);
     float c = 0.f;
 #pragma unroll
@@ -338,11 +340,16 @@ size_t b256(size_t x) { return (x + 255) / 256 * 256; }
 bool bal_al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t bal_es(int dt) { return dt == FWPKM_BF16 ? 2 : 4; }
 
-// Rows per CTA of the forward: about two CTAs of BL_THREADS per SM over all groups, and at
-// least 16 rows each (a CTA costs a row of partial sums).
+// CTAs that the GPU holds at once: a row of up to 1024 logits sits in the registers of a warp
+// twice (its values and the next row's loads).
+int bal_resident(int E) { return 148 * (E > 512 ? 2 : E > 256 ? 3 : 4); }
+
+// Rows per CTA of the forward: no more CTAs over all groups than are resident (a second wave of
+// a few doubles the time: 123 us instead of 70 for 16 groups of 4096 x 1024 fp32), and at
+// least 32 rows each (a CTA costs a row of partial sums).
 void split_rows(const fwpkm_balance_config& c, int* ctas, long long* rows) {
-  long long n = (2 * 148 + c.groups - 1) / c.groups;
-  const long long most = (c.tokens + 15) / 16;
+  long long n = bal_resident(c.experts) / c.groups;
+  const long long most = (c.tokens + 31) / 32;
   if (n > most) n = most;
   if (n < 1) n = 1;
   *rows = (c.tokens + n - 1) / n;
@@ -412,7 +419,8 @@ bool bal_go(const BalRun& r) {
   } else {
     constexpr int TEAMS = BL_THREADS / L;
     long long gx = (r.a.T + TEAMS - 1) / TEAMS;
-    const long long most = (4 * 148 + r.a.G - 1) / r.a.G;
+    const int all = bal_resident(r.a.E) / r.a.G;
+    const long long most = all < 1 ? 1 : all;
     if (gx > most) gx = most;
     launch_k(balance_grad_kernel<T, VEC, NCH, L>, dim3((unsigned)gx, r.a.G), BL_THREADS, 0, r.s, r.a, r.slope,
              r.d_loss, (T*)r.dx);
@@ -433,7 +441,7 @@ bool bal_shape(const BalRun& r) {
   if (VEC < 8 && v <= 256) return bal_go<T, VEC, 8, 32>(r);
   if (VEC > 1) return bal_go<T, VEC, (BL_MAX_E / VEC + BL_THREADS - 1) / BL_THREADS, BL_THREADS>(r);
   if (v <= 1024) return bal_go<T, VEC, VEC == 1 ? 32 : 1, 32>(r);
-  return bal_go<T, VEC, 8, BL_THREADS>(r);
+  return bal_go<T, VEC, VEC == 1 ? BL_MAX_E / BL_THREADS : 1, BL_THREADS>(r);
 }
 
 template <typename T>

@@ -283,7 +283,9 @@ struct ScanShape {
 // Column quads per CTA: as wide as 16 rows per thread allow; narrower tiles when the heads
 // alone do not fill the GPU and the tokens are too few to split (each tile re-reads q and k).
 ScanShape scan_shape(const ScanArgs& a) {
-  int lj = SC_THREADS * 16 / (pow2_ceil(a.d) < 16 ? 16 : pow2_ceil(a.d));
+  // (few tokens: 8 rows, so that more CTAs of a bandwidth-bound pass are resident)
+  const int rows = a.T <= SC_TB ? 8 : 16;
+  int lj = SC_THREADS * rows / (pow2_ceil(a.d) < 16 ? 16 : pow2_ceil(a.d));
   if (lj > 32) lj = 32;
   const int need = pow2_ceil((a.dv + 3) / 4);
   if (lj > need) lj = need < 4 ? 4 : need;

@@ -345,10 +345,15 @@ sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint3
   for (int b = threadIdx.x; b < bins; b += RS_THREADS) {
     uint32_t tot = 0, bef = 0;
     if (own_scan) {
-      for (int t = 0; t < tiles; ++t) {
-        const uint32_t c = hist[(long long)t * bins + b];
-        if (t == tile) bef = tot;
-        tot += c;
+      for (int t8 = 0; t8 < tiles; t8 += 8) {
+        uint32_t c[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) c[u] = t8 + u < tiles ? hist[(long long)(t8 + u) * bins + b] : 0u;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (t8 + u == tile) bef = tot;
+          tot += c[u];
+        }
       }
     } else {
       tot = total[b];
@@ -436,7 +441,6 @@ sort_small_kernel(const I* __restrict__ idx, int P, long long rows, int bits, in
 // reads to SEG terms plus its partials.
 // ---------------------------------------------------------------------------
 constexpr int SEG = 32;
-constexpr int SEG_U = 8;  // pairs in flight per team
 
 struct SegArgs {
   const uint32_t* key;
@@ -450,18 +454,30 @@ struct SegArgs {
   long long ranges;
 };
 
+// A team thread's columns of a row of d_table, in 16-byte accesses (or one element).
 template <typename G, int VEC>
-__device__ __forceinline__ void put_row(G* d_table, const SegArgs& a, uint32_t row, int c, const float (&acc)[VEC]) {
+struct GRow {
+  static constexpr int GV = (sizeof(G) * VEC > 16) ? 16 / (int)sizeof(G) : VEC;
+  Pack<G, GV> p[VEC / GV];
+  __device__ __forceinline__ void load(const G* d_table, const SegArgs& a, uint32_t row, int c) {
+    const G* src = d_table + (long long)row * a.grad_ld + (long long)c * VEC;
+#pragma unroll
+    for (int h = 0; h < VEC / GV; ++h) p[h] = *reinterpret_cast<const Pack<G, GV>*>(src + h * GV);
+  }
+};
+
+template <typename G, int VEC, bool ACC>
+__device__ __forceinline__ void put_row(G* d_table, const SegArgs& a, uint32_t row, int c, const float (&acc)[VEC],
+                                        const GRow<G, VEC>& old) {
   G* dst = d_table + (long long)row * a.grad_ld + (long long)c * VEC;
-  constexpr int GV = (sizeof(G) * VEC > 16) ? 16 / (int)sizeof(G) : VEC;  // elements per 16-byte access
+  constexpr int GV = GRow<G, VEC>::GV;
 #pragma unroll
   for (int h = 0; h < VEC / GV; ++h) {
     Pack<G, GV> y;
-    if (a.accumulate) y = *reinterpret_cast<const Pack<G, GV>*>(dst + h * GV);
 #pragma unroll
     for (int e = 0; e < GV; ++e) {
       const float s = acc[h * GV + e] * a.scale;
-      y.v[e] = from_f<G>(a.accumulate ? to_f<G>(y.v[e]) + s : s);
+      y.v[e] = from_f<G>(ACC ? to_f<G>(old.p[h].v[e]) + s : s);
     }
     *reinterpret_cast<Pack<G, GV>*>(dst + h * GV) = y;
   }
@@ -478,7 +494,8 @@ __device__ __forceinline__ bool has_row(const uint32_t* __restrict__ key, long l
   return lo < P && __ldg(key + lo) == row;
 }
 
-template <typename T, typename G, int VEC>
+// ACC: added to d_table, whose rows are loaded with the pairs (SEG_U pairs in flight per team).
+template <typename T, typename G, int VEC, bool ACC>
 __global__ void __launch_bounds__(LK_THREADS)
 lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_table, int sum_blocks) {
   pdl_wait();
@@ -512,6 +529,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   const long long range = (long long)blockIdx.x * ty_n + ty;
   if (c >= a.vecs || range >= a.ranges) return;
   const long long p0 = range * SEG, p1 = p0 + SEG < a.P ? p0 + SEG : a.P;
+  constexpr int SEG_U = ACC && VEC * sizeof(G) > 16 ? 4 : 8;
   const uint32_t none = (uint32_t)a.rows;
   float acc[VEC];
 #pragma unroll
@@ -520,24 +538,34 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   const bool cut_start = p0 > 0 && a.key[p0 - 1] == cur;
   const bool cut_end = p1 < a.P && a.key[p1] == a.key[p1 - 1];
   bool first = true;  // still in the range's first row
+  GRow<G, VEC> last;  // (accumulate) the row of the pair before, if it was its row's last
   for (long long q0 = p0; q0 < p1; q0 += SEG_U) {
     uint32_t k[SEG_U];
     float f[SEG_U];
     Pack<T, VEC> x[SEG_U];
+    uint32_t pr[SEG_U];
 #pragma unroll
     for (int u = 0; u < SEG_U; ++u) {
       const long long p = q0 + u;
       k[u] = p < p1 ? a.key[p] : none;
+      pr[u] = p < p1 ? a.pos[p] : 0u;
+    }
+    const uint32_t after = q0 + SEG_U < p1 ? a.key[q0 + SEG_U] : none;
+    GRow<G, VEC> old[SEG_U];
+#pragma unroll
+    for (int u = 0; u < SEG_U; ++u) {
       f[u] = 0.f;
       if (k[u] != none) {
-        const uint32_t pr = a.pos[p];
-        f[u] = a.w ? __ldg(a.w + pr) : 1.f;
-        x[u] = *reinterpret_cast<const Pack<T, VEC>*>(d_out + (long long)(pr / a.R) * a.out_ld + (long long)c * VEC);
+        f[u] = a.w ? __ldg(a.w + pr[u]) : 1.f;
+        x[u] = *reinterpret_cast<const Pack<T, VEC>*>(d_out + (long long)(pr[u] / a.R) * a.out_ld + (long long)c * VEC);
+        // the row's last pair here: what the gradient is added to, loaded with the pairs
+        if (ACC && k[u] != (u + 1 < SEG_U ? k[(u + 1) % SEG_U] : after)) old[u].load(d_table, a, k[u], c);
       }
     }
 #pragma unroll
     for (int u = 0; u < SEG_U; ++u) {
       if (q0 + u < p1) {
+        if (ACC && u > 0) last = old[(u + SEG_U - 1) % SEG_U];
         if (k[u] != cur) {
           if (cur != none) {
             if (first && cut_start) {
@@ -545,7 +573,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
 #pragma unroll
               for (int e = 0; e < VEC; ++e) d[e] = acc[e];
             } else {
-              put_row<G, VEC>(d_table, a, cur, c, acc);
+              put_row<G, VEC, ACC>(d_table, a, cur, c, acc, last);
             }
           }
 #pragma unroll
@@ -557,6 +585,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
 #pragma unroll
           for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f[u], to_f<T>(x[u].v[e]), acc[e]);
         }
+        if (ACC && (u == SEG_U - 1 || q0 + u + 1 == p1)) last = old[u];
       }
     }
   }
@@ -567,12 +596,12 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
 #pragma unroll
     for (int e = 0; e < VEC; ++e) d[e] = acc[e];
   } else {
-    put_row<G, VEC>(d_table, a, cur, c, acc);
+    put_row<G, VEC, ACC>(d_table, a, cur, c, acc, last);
   }
 }
 
 // Rows cut by range ends: the team of the range where the row begins adds its partials.
-template <typename G, int VEC>
+template <typename G, int VEC, bool ACC>
 __global__ void __launch_bounds__(LK_THREADS)
 lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
   pdl_wait();
@@ -609,7 +638,9 @@ lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] += x[u][e];
   }
-  put_row<G, VEC>(d_table, a, row, c, acc);
+  GRow<G, VEC> old;
+  if (ACC) old.load(d_table, a, row, c);
+  put_row<G, VEC, ACC>(d_table, a, row, c, acc, old);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -744,7 +775,7 @@ int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const Ba
   return nl;
 }
 
-template <typename T, typename G, int VEC>
+template <typename T, typename G, int VEC, bool ACC>
 int go_sum(const fwpkm_lookup_config& c, SegArgs a, const void* d_out, void* d_table, cudaStream_t s) {
   a.vecs = c.width / VEC;
   a.tx_n = row_threads(a.vecs);
@@ -754,39 +785,45 @@ int go_sum(const fwpkm_lookup_config& c, SegArgs a, const void* d_out, void* d_t
   // dense gradient: CTAs that zero the rows nothing reads, up to four per SM, each at least
   // 8 warps x 32 rows (column blocks share one row split: only blockIdx.y == 0 has them)
   long long zb = 0;
-  if (!a.accumulate) {
+  if (!ACC) {
     zb = (a.rows + 255) / 256;
     if (zb > 148 * 4) zb = 148 * 4;
   }
   if (sb + zb == 0) return 0;
   int nl = 0;
   if (gy == 1) {
-    launch_k(lookup_sum_kernel<T, G, VEC>, dim3(sb + (unsigned)zb), LK_THREADS, 0, s, a, (const T*)d_out,
+    launch_k(lookup_sum_kernel<T, G, VEC, ACC>, dim3(sb + (unsigned)zb), LK_THREADS, 0, s, a, (const T*)d_out,
              (G*)d_table, (int)sb);
     ++nl;
   } else {
     if (zb) {
-      launch_k(lookup_sum_kernel<T, G, VEC>, dim3((unsigned)zb), LK_THREADS, 0, s, a, (const T*)d_out, (G*)d_table, 0);
+      launch_k(lookup_sum_kernel<T, G, VEC, ACC>, dim3((unsigned)zb), LK_THREADS, 0, s, a, (const T*)d_out, (G*)d_table, 0);
       ++nl;
     }
     if (sb) {
-      launch_k(lookup_sum_kernel<T, G, VEC>, dim3(sb, gy), LK_THREADS, 0, s, a, (const T*)d_out, (G*)d_table,
+      launch_k(lookup_sum_kernel<T, G, VEC, ACC>, dim3(sb, gy), LK_THREADS, 0, s, a, (const T*)d_out, (G*)d_table,
                (int)sb);
       ++nl;
     }
   }
   if (a.ranges > 1) {
-    launch_k(lookup_join_kernel<G, VEC>, dim3(sb, gy), LK_THREADS, 0, s, a, (G*)d_table);
+    launch_k(lookup_join_kernel<G, VEC, ACC>, dim3(sb, gy), LK_THREADS, 0, s, a, (G*)d_table);
     ++nl;
   }
   return nl;
 }
 
+template <typename T, typename G, int VEC>
+int go_sum_a(const fwpkm_lookup_config& c, const SegArgs& a, const void* d_out, void* d_table, cudaStream_t s) {
+  return a.accumulate ? go_sum<T, G, VEC, true>(c, a, d_out, d_table, s)
+                      : go_sum<T, G, VEC, false>(c, a, d_out, d_table, s);
+}
+
 template <typename T, typename G>
 int go_sum_v(const fwpkm_lookup_config& c, const SegArgs& a, const void* d_out, void* d_table, cudaStream_t s) {
   if (rows_vec<T>(d_out, c.out_ld, c.width) && rows_vec<G>(d_table, a.grad_ld, c.width))
-    return go_sum<T, G, 16 / (int)sizeof(T)>(c, a, d_out, d_table, s);
-  return go_sum<T, G, 1>(c, a, d_out, d_table, s);
+    return go_sum_a<T, G, 16 / (int)sizeof(T)>(c, a, d_out, d_table, s);
+  return go_sum_a<T, G, 1>(c, a, d_out, d_table, s);
 }
 
 template <typename T, typename I, int VEC>
