@@ -12,6 +12,8 @@
 // gradient reads dout once per pair and writes (or updates) every row of dtable once.
 // No float atomics: the (row, pair) list is sorted by row with a stable radix sort, so each
 // row's terms are summed in pair order and the results are deterministic.
+#include <cooperative_groups.h>
+
 #include <cstdio>
 
 #include "fwpkm_internal.cuh"
@@ -133,33 +135,36 @@ lookup_bag_kernel(const T* __restrict__ table, long long rows, long long ld, con
 
 // dw: one warp per (token, DW_U ranks): the token's dout vectors are loaded once for them.
 constexpr int DW_U = 4;
+struct DwArgs {
+  const void* table;
+  const void* d_out;
+  float* dw;           // null: not wanted
+  long long rows, ld, out_ld, n;
+  int R, vecs;
+  float scale;
+};
 template <typename T, typename I, int VEC>
-__global__ void __launch_bounds__(LK_THREADS)
-lookup_dw_kernel(const T* __restrict__ table, long long rows, long long ld, const I* __restrict__ idx,
-                 const T* __restrict__ d_out, long long out_ld, long long n, int R, int vecs, float scale,
-                 float* __restrict__ dw) {
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int groups = (R + DW_U - 1) / DW_U;
-  const long long job = (long long)blockIdx.x * (LK_THREADS / 32) + (threadIdx.x >> 5);
+__device__ __forceinline__ void dw_job(const DwArgs& a, const I* __restrict__ idx, long long job, int lane) {
+  const T* table = (const T*)a.table;
+  const T* d_out = (const T*)a.d_out;
+  const int groups = (a.R + DW_U - 1) / DW_U;
   const long long t = job / groups;
-  if (t >= n) return;
+  if (t >= a.n) return;
   const int r0 = (int)(job - t * groups) * DW_U;
   long long row[DW_U];
   float acc[DW_U];
 #pragma unroll
   for (int u = 0; u < DW_U; ++u) {
-    row[u] = r0 + u < R ? load_idx(idx, t * R + r0 + u) : -1;
-    if (row[u] >= rows) row[u] = -1;
+    row[u] = r0 + u < a.R ? load_idx(idx, t * a.R + r0 + u) : -1;
+    if (row[u] >= a.rows) row[u] = -1;
     acc[u] = 0.f;
   }
-  for (int c = lane; c < vecs; c += 32) {
-    const Pack<T, VEC> g = *reinterpret_cast<const Pack<T, VEC>*>(d_out + t * out_ld + (long long)c * VEC);
+  for (int c = lane; c < a.vecs; c += 32) {
+    const Pack<T, VEC> g = *reinterpret_cast<const Pack<T, VEC>*>(d_out + t * a.out_ld + (long long)c * VEC);
     Pack<T, VEC> x[DW_U];
 #pragma unroll
     for (int u = 0; u < DW_U; ++u)
-      if (row[u] >= 0) x[u] = *reinterpret_cast<const Pack<T, VEC>*>(table + row[u] * ld + (long long)c * VEC);
+      if (row[u] >= 0) x[u] = *reinterpret_cast<const Pack<T, VEC>*>(table + row[u] * a.ld + (long long)c * VEC);
 #pragma unroll
     for (int u = 0; u < DW_U; ++u)
       if (row[u] >= 0) {
@@ -172,8 +177,15 @@ lookup_dw_kernel(const T* __restrict__ table, long long rows, long long ld, cons
   if (lane == 0) {
 #pragma unroll
     for (int u = 0; u < DW_U; ++u)
-      if (r0 + u < R) dw[t * R + r0 + u] = row[u] >= 0 ? acc[u] * scale : 0.f;
+      if (r0 + u < a.R) a.dw[t * a.R + r0 + u] = row[u] >= 0 ? acc[u] * a.scale : 0.f;
   }
+}
+template <typename T, typename I, int VEC>
+__global__ void __launch_bounds__(LK_THREADS)
+lookup_dw_kernel(DwArgs a, const I* __restrict__ idx) {
+  pdl_wait();
+  pdl_trigger();
+  dw_job<T, I, VEC>(a, idx, (long long)blockIdx.x * (LK_THREADS / 32) + (threadIdx.x >> 5), threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------------------
@@ -249,9 +261,10 @@ sort_scan_kernel(uint32_t* __restrict__ hist, uint32_t* __restrict__ total, int 
   total[b] = run;
 }
 
-// Exclusive sum over `bins` values in shared memory (bins <= RS_MAX_BINS, RS_THREADS threads).
+// Exclusive sum over `bins` values in shared memory (bins <= MAXB, THREADS threads).
+template <int THREADS, int MAXB>
 __device__ __forceinline__ void block_exclusive(uint32_t* s, int bins, uint32_t* warp_tot) {
-  constexpr int PER = RS_MAX_BINS / RS_THREADS;
+  constexpr int PER = MAXB / THREADS < 1 ? 1 : MAXB / THREADS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x[PER], sum = 0;
 #pragma unroll
@@ -269,7 +282,8 @@ __device__ __forceinline__ void block_exclusive(uint32_t* s, int bins, uint32_t*
   if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
   uint32_t before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_tot[w];
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) before += w < warp ? warp_tot[w] : 0u;
   uint32_t run = before + inc - sum;
   __syncthreads();
 #pragma unroll
@@ -281,20 +295,27 @@ __device__ __forceinline__ void block_exclusive(uint32_t* s, int bins, uint32_t*
   __syncthreads();
 }
 
-// Stable ranks of a tile's items inside their bins: warp w holds items [w, w+1) * 32 RS_ITEMS
+// Stable ranks of a tile's items inside their bins: warp w holds items [w, w+1) * 32 ITEMS
 // of the tile in order, 32 at a time; lanes with equal digits rank each other by lane.
 // wh[warp][bin] (uint16) ends as the number of earlier items of the tile in the bin from
-// earlier warps; rank[i] counts those of the same warp.
-__device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[RS_ITEMS], const bool (&live)[RS_ITEMS],
-                                           uint16_t* wh, int bins, uint32_t (&rank)[RS_ITEMS]) {
+// earlier warps, count[bin] (if given) as the tile's; rank[i] counts those of the same warp.
+template <int WARPS, int ITEMS>
+__device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[ITEMS], const bool (&live)[ITEMS], uint16_t* wh,
+                                           int bins, uint32_t (&rank)[ITEMS], uint32_t* count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int b = threadIdx.x; b < bins * RS_WARPS / 2; b += RS_THREADS) reinterpret_cast<uint32_t*>(wh)[b] = 0u;
+  for (int b = threadIdx.x; b < bins * WARPS / 2; b += WARPS * 32) reinterpret_cast<uint32_t*>(wh)[b] = 0u;
   __syncthreads();
   uint16_t* mine = wh + (size_t)warp * bins;
 #pragma unroll
-  for (int i = 0; i < RS_ITEMS; ++i) {
-    const uint32_t d = live[i] ? digit[i] : 0xffffffffu;
-    const unsigned peers = __match_any_sync(0xffffffffu, d);
+  for (int i = 0; i < ITEMS; ++i) {
+    // lanes with the same digit, bit by bit (a match instruction over the warp is slower)
+    unsigned peers = __ballot_sync(0xffffffffu, live[i]);
+    if (!live[i]) peers = ~peers;
+    for (int b = 0; (1 << b) < bins; ++b) {
+      const bool set = (digit[i] >> b) & 1u;
+      const unsigned with = __ballot_sync(0xffffffffu, set);
+      peers &= set ? with : ~with;
+    }
     const unsigned below = __popc(peers & ((1u << lane) - 1u));
     uint32_t old = 0;
     if (live[i]) old = mine[digit[i]];
@@ -304,14 +325,20 @@ __device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[RS_ITEMS], co
     rank[i] = old + below;
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += RS_THREADS) {
+  for (int b = threadIdx.x; b < bins; b += WARPS * 32) {
     uint32_t run = 0;
 #pragma unroll
-    for (int w = 0; w < RS_WARPS; ++w) {
-      const uint32_t c = wh[(size_t)w * bins + b];
-      wh[(size_t)w * bins + b] = (uint16_t)run;
-      run += c;
+    for (int w8 = 0; w8 < WARPS; w8 += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) c[u] = wh[(size_t)(w8 + u) * bins + b];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        wh[(size_t)(w8 + u) * bins + b] = (uint16_t)run;
+        run += c[u];
+      }
     }
+    if (count) count[b] = run;
   }
   __syncthreads();
 }
@@ -363,8 +390,8 @@ sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint3
     before[b] = bef;
   }
   __syncthreads();
-  block_exclusive(base, bins, warp_tot);
-  tile_ranks(digit, live, wh, bins, rank);
+  block_exclusive<RS_THREADS, RS_MAX_BINS>(base, bins, warp_tot);
+  tile_ranks<RS_WARPS, RS_ITEMS>(digit, live, wh, bins, rank, nullptr);
 #pragma unroll
   for (int i = 0; i < RS_ITEMS; ++i)
     if (live[i]) {
@@ -375,60 +402,89 @@ sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint3
     }
 }
 
-// Up to one tile of pairs: the whole sort in one CTA, the passes through shared memory.
-template <typename I>
-__global__ void __launch_bounds__(RS_THREADS)
-sort_small_kernel(const I* __restrict__ idx, int P, long long rows, int bits, int passes,
-                  uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out) {
-  extern __shared__ uint32_t sm[];
-  const int per = (bits + passes - 1) / passes, bins = 1 << per;
-  uint32_t* sk = sm;                                // [RS_TILE]
-  uint32_t* sp = sm + RS_TILE;                      // [RS_TILE]
-  uint32_t* base = sp + RS_TILE;                    // [bins]
-  uint16_t* wh = (uint16_t*)(base + bins);          // [RS_WARPS][bins]
-  __shared__ uint32_t warp_tot[RS_WARPS];
+// Up to CS_MAX pairs: the whole sort in one launch, by one cluster of up to eight CTAs that
+// keeps the pairs in its shared memory (each pass: ranks in the CTA's tile, the tiles' counts
+// read from one another, the items stored to their place in whichever CTA holds it).  The
+// launch's other clusters form dw meanwhile, which needs no sorting.  (The launches of the
+// general sort took 40 us for 16384 pairs, most of it latency.)
+constexpr int CS_THREADS = 1024, CS_WARPS = CS_THREADS / 32, CS_ITEMS = 8, CS_TILE = CS_THREADS * CS_ITEMS;
+constexpr int CS_BITS = 9, CS_MAX_BINS = 1 << CS_BITS, CS_CLUSTER = 8;
+constexpr long long CS_MAX = (long long)CS_TILE * CS_CLUSTER;
+constexpr size_t CS_SMEM = 8 * (size_t)CS_TILE + 4 * 3 * (size_t)CS_MAX_BINS + 2 * (size_t)CS_WARPS * CS_MAX_BINS;
+
+template <typename T, typename I, int VEC>
+__global__ void __launch_bounds__(CS_THREADS, 1)
+sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, int passes, int ctas,
+                    uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out, DwArgs dw) {
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint8_t cs_raw[];
+  uint2* item = (uint2*)cs_raw;                              // [CS_TILE] (key, pair)
+  uint32_t* count = (uint32_t*)(item + CS_TILE);             // [CS_MAX_BINS] this tile's
+  uint32_t* base = count + CS_MAX_BINS;                      // [CS_MAX_BINS]
+  uint32_t* before = base + CS_MAX_BINS;                     // [CS_MAX_BINS] earlier tiles'
+  uint16_t* wh = (uint16_t*)(before + CS_MAX_BINS);          // [CS_WARPS][bins]
+  __shared__ uint32_t warp_tot[CS_WARPS];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t key[RS_ITEMS], pos[RS_ITEMS], digit[RS_ITEMS], rank[RS_ITEMS];
-  bool live[RS_ITEMS];
+  if ((int)blockIdx.x >= ctas) {
+    const long long jobs = dw.n * ((dw.R + DW_U - 1) / DW_U);
+    const long long step = (long long)(gridDim.x - ctas) * CS_WARPS;
+    for (long long j = (long long)(blockIdx.x - ctas) * CS_WARPS + warp; j < jobs; j += step)
+      dw_job<T, I, VEC>(dw, idx, j, lane);
+    return;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tile = blockIdx.x, bins = 1 << per;
+  uint32_t key[CS_ITEMS], pos[CS_ITEMS], digit[CS_ITEMS], rank[CS_ITEMS];
+  bool live[CS_ITEMS];
 #pragma unroll
-  for (int i = 0; i < RS_ITEMS; ++i) {
-    const int p = (warp * RS_ITEMS + i) * 32 + lane;
+  for (int i = 0; i < CS_ITEMS; ++i) {
+    const int p = tile * CS_TILE + (warp * CS_ITEMS + i) * 32 + lane;
     live[i] = p < P;
     key[i] = live[i] ? pair_key(idx, p, rows) : 0u;
     pos[i] = (uint32_t)p;
   }
   for (int pass = 0; pass < passes; ++pass) {
-    for (int b = threadIdx.x; b < bins; b += RS_THREADS) base[b] = 0u;
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < RS_ITEMS; ++i) {
-      digit[i] = (key[i] >> (pass * per)) & (bins - 1);
-      if (live[i]) atomicAdd(&base[digit[i]], 1u);
+    for (int i = 0; i < CS_ITEMS; ++i) digit[i] = (key[i] >> (pass * per)) & (bins - 1);
+    tile_ranks<CS_WARPS, CS_ITEMS>(digit, live, wh, bins, rank, count);
+    cluster.sync();  // every tile's counts are there, and its items in registers
+    if ((int)threadIdx.x < bins) {
+      uint32_t tot = 0, bef = 0;
+#pragma unroll
+      for (int r = 0; r < CS_CLUSTER; ++r) {
+        const uint32_t c = r < ctas ? cluster.map_shared_rank(count, r < ctas ? r : 0)[threadIdx.x] : 0u;
+        if (r < tile) bef += c;
+        tot += c;
+      }
+      base[threadIdx.x] = tot;
+      before[threadIdx.x] = bef;
     }
     __syncthreads();
-    block_exclusive(base, bins, warp_tot);
-    tile_ranks(digit, live, wh, bins, rank);
+    block_exclusive<CS_THREADS, CS_MAX_BINS>(base, bins, warp_tot);
     const bool last = pass == passes - 1;
 #pragma unroll
-    for (int i = 0; i < RS_ITEMS; ++i)
+    for (int i = 0; i < CS_ITEMS; ++i)
       if (live[i]) {
-        const uint32_t at = base[digit[i]] + wh[(size_t)warp * bins + digit[i]] + rank[i];
-        (last ? key_out : sk)[at] = key[i];
-        (last ? pos_out : sp)[at] = pos[i];
-      }
-    __syncthreads();
-    if (!last) {
-#pragma unroll
-      for (int i = 0; i < RS_ITEMS; ++i) {
-        const int p = (warp * RS_ITEMS + i) * 32 + lane;
-        if (live[i]) {
-          key[i] = sk[p];
-          pos[i] = sp[p];
+        const uint32_t d = digit[i];
+        const uint32_t at = base[d] + before[d] + wh[(size_t)warp * bins + d] + rank[i];
+        if (last) {
+          key_out[at] = key[i];
+          pos_out[at] = pos[i];
+        } else {
+          cluster.map_shared_rank(item, at / CS_TILE)[at % CS_TILE] = make_uint2(key[i], pos[i]);
         }
       }
-      __syncthreads();
+    cluster.sync();  // the items are in place (last pass: nobody reads this tile's counts any more)
+    if (!last) {
+#pragma unroll
+      for (int i = 0; i < CS_ITEMS; ++i)
+        if (live[i]) {
+          const uint2 x = item[(warp * CS_ITEMS + i) * 32 + lane];
+          key[i] = x.x;
+          pos[i] = x.y;
+        }
     }
   }
 }
@@ -483,6 +539,30 @@ __device__ __forceinline__ void put_row(G* d_table, const SegArgs& a, uint32_t r
   }
 }
 
+// A team thread's columns of a partial sum (VEC > 1: the width is a multiple of VEC >= 4, so
+// they lie on the 16-byte grid).
+template <int VEC>
+__device__ __forceinline__ void put_part(float* d, const float (&x)[VEC]) {
+  constexpr int W = VEC < 4 ? 1 : 4;
+#pragma unroll
+  for (int e = 0; e < VEC; e += W) {
+    Pack<float, W> y;
+#pragma unroll
+    for (int u = 0; u < W; ++u) y.v[u] = x[e + u];
+    *reinterpret_cast<Pack<float, W>*>(d + e) = y;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void get_part(const float* d, float (&x)[VEC]) {
+  constexpr int W = VEC < 4 ? 1 : 4;
+#pragma unroll
+  for (int e = 0; e < VEC; e += W) {
+    const Pack<float, W> y = *reinterpret_cast<const Pack<float, W>*>(d + e);
+#pragma unroll
+    for (int u = 0; u < W; ++u) x[e + u] = y.v[u];
+  }
+}
+
 // Whether `row` occurs in the sorted keys.
 __device__ __forceinline__ bool has_row(const uint32_t* __restrict__ key, long long P, uint32_t row) {
   long long lo = 0, hi = P;
@@ -496,7 +576,7 @@ __device__ __forceinline__ bool has_row(const uint32_t* __restrict__ key, long l
 
 // ACC: added to d_table, whose rows are loaded with the pairs (SEG_U pairs in flight per team).
 template <typename T, typename G, int VEC, bool ACC>
-__global__ void __launch_bounds__(LK_THREADS)
+__global__ void __launch_bounds__(LK_THREADS, 2)
 lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_table, int sum_blocks) {
   pdl_wait();
   pdl_trigger();
@@ -529,7 +609,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   const long long range = (long long)blockIdx.x * ty_n + ty;
   if (c >= a.vecs || range >= a.ranges) return;
   const long long p0 = range * SEG, p1 = p0 + SEG < a.P ? p0 + SEG : a.P;
-  constexpr int SEG_U = ACC && VEC * sizeof(G) > 16 ? 4 : 8;
+  constexpr int SEG_U = ACC && VEC == 8 ? 4 : 8;
   const uint32_t none = (uint32_t)a.rows;
   float acc[VEC];
 #pragma unroll
@@ -569,9 +649,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
         if (k[u] != cur) {
           if (cur != none) {
             if (first && cut_start) {
-              float* d = a.part + (range * 2) * a.width + (long long)c * VEC;
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) d[e] = acc[e];
+              put_part<VEC>(a.part + (range * 2) * a.width + (long long)c * VEC, acc);
             } else {
               put_row<G, VEC, ACC>(d_table, a, cur, c, acc, last);
             }
@@ -592,9 +670,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   if (cur == none) return;
   if ((first && cut_start) || cut_end) {
     // a row cut at both ends is one partial, kept as the start's
-    float* d = a.part + (range * 2 + ((first && cut_start) ? 0 : 1)) * a.width + (long long)c * VEC;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) d[e] = acc[e];
+    put_part<VEC>(a.part + (range * 2 + ((first && cut_start) ? 0 : 1)) * a.width + (long long)c * VEC, acc);
   } else {
     put_row<G, VEC, ACC>(d_table, a, cur, c, acc, last);
   }
@@ -623,20 +699,19 @@ lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
     else hi = mid;
   }
   float acc[VEC];
-  const float* d = a.part + (range * 2 + 1) * a.width + (long long)c * VEC;
+  get_part<VEC>(a.part + (range * 2 + 1) * a.width + (long long)c * VEC, acc);
+  constexpr int U = VEC > 4 ? 4 : 8;
+  for (long long q0 = range + 1; q0 < lo; q0 += U) {
+    float x[U][VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = d[e];
-  for (long long q0 = range + 1; q0 < lo; q0 += 8) {
-    float x[8][VEC];
+    for (int u = 0; u < U; ++u)
+      if (q0 + u < lo) get_part<VEC>(a.part + ((q0 + u) * 2) * a.width + (long long)c * VEC, x[u]);
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u = 0; u < U; ++u)
+      if (q0 + u < lo) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        x[u][e] = q0 + u < lo ? a.part[((q0 + u) * 2) * a.width + (long long)c * VEC + e] : 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] += x[u][e];
+        for (int e = 0; e < VEC; ++e) acc[e] += x[u][e];
+      }
   }
   GRow<G, VEC> old;
   if (ACC) old.load(d_table, a, row, c);
@@ -742,15 +817,50 @@ void go_lookup_v(const fwpkm_lookup_config& c, const void* table, const void* id
     go_lookup<T, I, 1>(c, table, idx, w, n, out, s);
 }
 
-template <typename I>
-int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const BackWork& w, int* sorted,
+// A launch in clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+void launch_cluster(void (*kern)(KArgs...), unsigned grid, unsigned block, unsigned cluster, size_t smem,
+                    cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr[2];
+  unsigned na = 0;
+  attr[na].id = cudaLaunchAttributeClusterDimension;
+  attr[na].val.clusterDim.x = cluster;
+  attr[na].val.clusterDim.y = 1;
+  attr[na++].val.clusterDim.z = 1;
+  if (pdl_enabled()) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+// The sorted pairs end in w.key / w.pos [*sorted].  Up to CS_MAX pairs: one launch, which forms
+// dw too (dw.dw is cleared to say so).
+template <typename T, typename I, int VEC>
+int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const BackWork& w, int* sorted, DwArgs* dw,
             cudaStream_t s) {
   const SortPlan sp = sort_plan(c.rows, P);
-  if (P <= RS_TILE) {
-    const size_t smem = 4 * (2 * (size_t)RS_TILE + sp.bins) + 2 * (size_t)RS_WARPS * sp.bins;
-    if (!raise_smem_limit((const void*)sort_small_kernel<I>, smem)) return -1;
-    launch_k(sort_small_kernel<I>, 1, RS_THREADS, smem, s, (const I*)idx, (int)P, c.rows, sp.bits, sp.passes,
-             w.key[0], w.pos[0]);
+  if (P <= CS_MAX) {
+    int ctas = 1;
+    while ((long long)ctas * CS_TILE < P) ctas <<= 1;
+    const int passes = (sp.bits + CS_BITS - 1) / CS_BITS, per = (sp.bits + passes - 1) / passes;
+    long long more = 0;
+    if (dw->dw) {
+      more = (dw->n * ((dw->R + DW_U - 1) / DW_U) + CS_WARPS - 1) / CS_WARPS;
+      if (more > 148 - ctas) more = 148 - ctas;
+      more = (more + ctas - 1) / ctas * ctas;
+    }
+    if (!raise_smem_limit((const void*)sort_cluster_kernel<T, I, VEC>, CS_SMEM)) return -1;
+    launch_cluster(sort_cluster_kernel<T, I, VEC>, (unsigned)(ctas + more), CS_THREADS, (unsigned)ctas, CS_SMEM, s,
+                   (const I*)idx, (int)P, c.rows, per, passes, ctas, w.key[0], w.pos[0], *dw);
+    dw->dw = nullptr;
     *sorted = 0;
     return 1;
   }
@@ -826,22 +936,34 @@ int go_sum_v(const fwpkm_lookup_config& c, const SegArgs& a, const void* d_out, 
   return go_sum_a<T, G, 1>(c, a, d_out, d_table, s);
 }
 
+// Sort (if there is a d_table to form) and dw, by the table's and the indices' types.
 template <typename T, typename I, int VEC>
-void go_dw(const fwpkm_lookup_config& c, const void* table, const void* idx, const void* d_out, long long n,
-           float* dw, cudaStream_t s) {
-  const long long jobs = n * ((c.R + DW_U - 1) / DW_U);
-  const unsigned g = (unsigned)((jobs + LK_THREADS / 32 - 1) / (LK_THREADS / 32));
-  launch_k(lookup_dw_kernel<T, I, VEC>, g, LK_THREADS, 0, s, (const T*)table, c.rows, c.table_ld, (const I*)idx,
-           (const T*)d_out, c.out_ld, n, c.R, c.width / VEC, c.scale, dw);
+int go_pairs(const fwpkm_lookup_config& c, const void* idx, long long P, const BackWork* w, int* sorted, DwArgs dw,
+             cudaStream_t s) {
+  dw.vecs = c.width / VEC;
+  int nl = 0;
+  if (w) {
+    nl = go_sort<T, I, VEC>(c, idx, P, *w, sorted, &dw, s);
+    if (nl < 0) return -1;
+  }
+  if (dw.dw) {
+    const long long jobs = dw.n * ((c.R + DW_U - 1) / DW_U);
+    const unsigned g = (unsigned)((jobs + LK_THREADS / 32 - 1) / (LK_THREADS / 32));
+    launch_k(lookup_dw_kernel<T, I, VEC>, g, LK_THREADS, 0, s, dw, (const I*)idx);
+    ++nl;
+  }
+  return nl;
 }
 
-template <typename T, typename I>
-void go_dw_v(const fwpkm_lookup_config& c, const void* table, const void* idx, const void* d_out, long long n,
-             float* dw, cudaStream_t s) {
-  if (rows_vec<T>(table, c.table_ld, c.width) && rows_vec<T>(d_out, c.out_ld, c.width))
-    go_dw<T, I, 16 / (int)sizeof(T)>(c, table, idx, d_out, n, dw, s);
-  else
-    go_dw<T, I, 1>(c, table, idx, d_out, n, dw, s);
+template <typename T>
+int go_pairs_t(const fwpkm_lookup_config& c, const void* idx, long long P, const BackWork* w, int* sorted,
+               const DwArgs& dw, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const bool vec = !dw.dw || (rows_vec<T>(dw.table, c.table_ld, c.width) && rows_vec<T>(dw.d_out, c.out_ld, c.width));
+  if (c.idx_dtype == FWPKM_I64)
+    return vec ? go_pairs<T, long long, V>(c, idx, P, w, sorted, dw, s)
+               : go_pairs<T, long long, 1>(c, idx, P, w, sorted, dw, s);
+  return vec ? go_pairs<T, int, V>(c, idx, P, w, sorted, dw, s) : go_pairs<T, int, 1>(c, idx, P, w, sorted, dw, s);
 }
 
 }  // namespace
@@ -906,9 +1028,19 @@ fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* t
   cudaStream_t s = (cudaStream_t)stream;
   cudaGetLastError();
   PdlScope pdl(true);
-  const bool i64 = cfg->idx_dtype == FWPKM_I64, bf = cfg->dtype == FWPKM_BF16;
+  const bool bf = cfg->dtype == FWPKM_BF16;
   const long long P = n * cfg->R;
-  int nl = 0;
+  BackWork bw = {};
+  int nl = 0, at = 0;
+  if (P > 0) {
+    if (d_table) back_carve(*cfg, P, (char*)workspace, &bw);
+    DwArgs g = {};
+    g.table = table; g.d_out = d_out; g.dw = dw;
+    g.rows = cfg->rows; g.ld = cfg->table_ld; g.out_ld = cfg->out_ld; g.n = n; g.R = cfg->R; g.scale = cfg->scale;
+    const BackWork* w = d_table ? &bw : nullptr;
+    nl = bf ? go_pairs_t<__nv_bfloat16>(*cfg, idx, P, w, &at, g, s) : go_pairs_t<float>(*cfg, idx, P, w, &at, g, s);
+    if (nl < 0) return FWPKM_ERR_CUDA;
+  }
   if (d_table) {
     SegArgs a = {};
     a.P = P;
@@ -916,32 +1048,15 @@ fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* t
     a.R = cfg->R; a.width = cfg->width; a.scale = cfg->scale; a.accumulate = accumulate != 0;
     a.ranges = (P + SEG - 1) / SEG;
     a.w = w;
-    if (P > 0) {
-      BackWork bw;
-      back_carve(*cfg, P, (char*)workspace, &bw);
-      int at = 0;
-      nl = i64 ? go_sort<long long>(*cfg, idx, P, bw, &at, s) : go_sort<int>(*cfg, idx, P, bw, &at, s);
-      if (nl < 0) return FWPKM_ERR_CUDA;
-      a.key = bw.key[at];
-      a.pos = bw.pos[at];
-      a.part = bw.part;
-    }
+    a.key = bw.key[at];
+    a.pos = bw.pos[at];
+    a.part = bw.part;
     if (bf)
       nl += grad_dtype == FWPKM_BF16 ? go_sum_v<__nv_bfloat16, __nv_bfloat16>(*cfg, a, d_out, d_table, s)
                                      : go_sum_v<__nv_bfloat16, float>(*cfg, a, d_out, d_table, s);
     else
       nl += grad_dtype == FWPKM_BF16 ? go_sum_v<float, __nv_bfloat16>(*cfg, a, d_out, d_table, s)
                                      : go_sum_v<float, float>(*cfg, a, d_out, d_table, s);
-  }
-  if (dw && n > 0) {
-    if (bf) {
-      if (i64) go_dw_v<__nv_bfloat16, long long>(*cfg, table, idx, d_out, n, dw, s);
-      else go_dw_v<__nv_bfloat16, int>(*cfg, table, idx, d_out, n, dw, s);
-    } else {
-      if (i64) go_dw_v<float, long long>(*cfg, table, idx, d_out, n, dw, s);
-      else go_dw_v<float, int>(*cfg, table, idx, d_out, n, dw, s);
-    }
-    ++nl;
   }
   return done(nl);
 }
