@@ -14,6 +14,7 @@
 // row's terms are summed in pair order and the results are deterministic.
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <cstdio>
 
 #include "fwpkm_internal.cuh"
@@ -213,11 +214,11 @@ __device__ __forceinline__ uint32_t pair_key(const I* idx, long long p, long lon
 template <typename I>
 struct Source {
   const I* idx;
-  const uint32_t* key;
-  const uint32_t* pos;
+  const uint2* item;  // (key, pair)
   long long rows;
-  __device__ __forceinline__ uint32_t k(long long p) const { return key ? key[p] : pair_key(idx, p, rows); }
-  __device__ __forceinline__ uint32_t v(long long p) const { return key ? pos[p] : (uint32_t)p; }
+  __device__ __forceinline__ uint2 at(long long p) const {
+    return item ? item[p] : make_uint2(pair_key(idx, p, rows), (uint32_t)p);
+  }
 };
 
 // Counts of one tile's digits: hist[tile][bin].
@@ -233,7 +234,7 @@ sort_hist_kernel(Source<I> src, long long P, int shift, int bins, uint32_t* __re
 #pragma unroll
   for (int i = 0; i < RS_ITEMS; ++i) {
     const long long p = base + i * RS_THREADS + threadIdx.x;
-    if (p < P) atomicAdd(&s[(src.k(p) >> shift) & (bins - 1)], 1u);
+    if (p < P) atomicAdd(&s[(src.at(p).x >> shift) & (bins - 1)], 1u);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += RS_THREADS) hist[(long long)blockIdx.x * bins + b] = s[b];
@@ -301,13 +302,14 @@ __device__ __forceinline__ void block_exclusive(uint32_t* s, int bins, uint32_t*
 // earlier warps, count[bin] (if given) as the tile's; rank[i] counts those of the same warp.
 template <int WARPS, int ITEMS>
 __device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[ITEMS], const bool (&live)[ITEMS], uint16_t* wh,
-                                           int bins, uint32_t (&rank)[ITEMS], uint32_t* count) {
+                                           int bins, uint32_t (&rank)[ITEMS], uint32_t* count, int items = ITEMS) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int b = threadIdx.x; b < bins * WARPS / 2; b += WARPS * 32) reinterpret_cast<uint32_t*>(wh)[b] = 0u;
   __syncthreads();
   uint16_t* mine = wh + (size_t)warp * bins;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
+    if (i >= items) break;
     // lanes with the same digit, bit by bit (a match instruction over the warp is slower)
     unsigned peers = __ballot_sync(0xffffffffu, live[i]);
     if (!live[i]) peers = ~peers;
@@ -348,8 +350,7 @@ __device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[ITEMS], const
 template <typename I>
 __global__ void __launch_bounds__(RS_THREADS)
 sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint32_t* __restrict__ hist,
-                    const uint32_t* __restrict__ total, int tiles, int own_scan, uint32_t* __restrict__ key_out,
-                    uint32_t* __restrict__ pos_out) {
+                    const uint32_t* __restrict__ total, int tiles, int own_scan, uint2* __restrict__ out) {
   extern __shared__ uint32_t sm[];
   uint32_t* base = sm;                              // [bins]
   uint32_t* before = sm + bins;                     // [bins] earlier tiles' items of the bin
@@ -365,8 +366,9 @@ sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint3
   for (int i = 0; i < RS_ITEMS; ++i) {
     const long long p = (long long)tile * RS_TILE + (warp * RS_ITEMS + i) * 32 + lane;
     live[i] = p < P;
-    key[i] = live[i] ? src.k(p) : 0u;
-    pos[i] = live[i] ? src.v(p) : 0u;
+    const uint2 x = live[i] ? src.at(p) : make_uint2(0u, 0u);
+    key[i] = x.x;
+    pos[i] = x.y;
     digit[i] = (key[i] >> shift) & (bins - 1);
   }
   for (int b = threadIdx.x; b < bins; b += RS_THREADS) {
@@ -396,26 +398,24 @@ sort_scatter_kernel(Source<I> src, long long P, int shift, int bins, const uint3
   for (int i = 0; i < RS_ITEMS; ++i)
     if (live[i]) {
       const uint32_t d = digit[i];
-      const uint32_t at = base[d] + before[d] + wh[(size_t)warp * bins + d] + rank[i];
-      key_out[at] = key[i];
-      pos_out[at] = pos[i];
+      out[base[d] + before[d] + wh[(size_t)warp * bins + d] + rank[i]] = make_uint2(key[i], pos[i]);
     }
 }
 
-// Up to CS_MAX pairs: the whole sort in one launch, by one cluster of up to eight CTAs that
+// Up to CS_MAX pairs: the whole sort in one launch, by one cluster of up to sixteen CTAs that
 // keeps the pairs in its shared memory (each pass: ranks in the CTA's tile, the tiles' counts
 // read from one another, the items stored to their place in whichever CTA holds it).  The
 // launch's other clusters form dw meanwhile, which needs no sorting.  (The launches of the
 // general sort took 40 us for 16384 pairs, most of it latency.)
 constexpr int CS_THREADS = 1024, CS_WARPS = CS_THREADS / 32, CS_ITEMS = 8, CS_TILE = CS_THREADS * CS_ITEMS;
-constexpr int CS_BITS = 9, CS_MAX_BINS = 1 << CS_BITS, CS_CLUSTER = 8;
-constexpr long long CS_MAX = (long long)CS_TILE * CS_CLUSTER;
+constexpr int CS_BITS = 9, CS_MAX_BINS = 1 << CS_BITS, CS_CLUSTER = 16;
+constexpr long long CS_MAX = (long long)CS_TILE * 8;  // eight CTAs hold them; sixteen, where a GPC has them, in half the time
 constexpr size_t CS_SMEM = 8 * (size_t)CS_TILE + 4 * 3 * (size_t)CS_MAX_BINS + 2 * (size_t)CS_WARPS * CS_MAX_BINS;
 
 template <typename T, typename I, int VEC>
 __global__ void __launch_bounds__(CS_THREADS, 1)
-sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, int passes, int ctas,
-                    uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out, DwArgs dw) {
+sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, int passes, int ctas, int items,
+                    uint2* __restrict__ out, DwArgs dw) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t cs_raw[];
   uint2* item = (uint2*)cs_raw;                              // [CS_TILE] (key, pair)
@@ -435,20 +435,20 @@ sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, i
     return;
   }
   cg::cluster_group cluster = cg::this_cluster();
-  const int tile = blockIdx.x, bins = 1 << per;
+  const int tile = blockIdx.x, bins = 1 << per, tile_items = items * CS_THREADS;  // `items` per thread
   uint32_t key[CS_ITEMS], pos[CS_ITEMS], digit[CS_ITEMS], rank[CS_ITEMS];
   bool live[CS_ITEMS];
 #pragma unroll
   for (int i = 0; i < CS_ITEMS; ++i) {
-    const int p = tile * CS_TILE + (warp * CS_ITEMS + i) * 32 + lane;
-    live[i] = p < P;
+    const int p = tile * tile_items + (warp * items + i) * 32 + lane;
+    live[i] = i < items && p < P;
     key[i] = live[i] ? pair_key(idx, p, rows) : 0u;
     pos[i] = (uint32_t)p;
   }
   for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll
     for (int i = 0; i < CS_ITEMS; ++i) digit[i] = (key[i] >> (pass * per)) & (bins - 1);
-    tile_ranks<CS_WARPS, CS_ITEMS>(digit, live, wh, bins, rank, count);
+    tile_ranks<CS_WARPS, CS_ITEMS>(digit, live, wh, bins, rank, count, items);
     cluster.sync();  // every tile's counts are there, and its items in registers
     if ((int)threadIdx.x < bins) {
       uint32_t tot = 0, bef = 0;
@@ -469,19 +469,16 @@ sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, i
       if (live[i]) {
         const uint32_t d = digit[i];
         const uint32_t at = base[d] + before[d] + wh[(size_t)warp * bins + d] + rank[i];
-        if (last) {
-          key_out[at] = key[i];
-          pos_out[at] = pos[i];
-        } else {
-          cluster.map_shared_rank(item, at / CS_TILE)[at % CS_TILE] = make_uint2(key[i], pos[i]);
-        }
+        const uint32_t cta = at / (uint32_t)tile_items;
+        if (last) out[at] = make_uint2(key[i], pos[i]);
+        else cluster.map_shared_rank(item, cta)[at - cta * tile_items] = make_uint2(key[i], pos[i]);
       }
     cluster.sync();  // the items are in place (last pass: nobody reads this tile's counts any more)
     if (!last) {
 #pragma unroll
       for (int i = 0; i < CS_ITEMS; ++i)
         if (live[i]) {
-          const uint2 x = item[(warp * CS_ITEMS + i) * 32 + lane];
+          const uint2 x = item[(warp * items + i) * 32 + lane];
           key[i] = x.x;
           pos[i] = x.y;
         }
@@ -499,8 +496,7 @@ sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, i
 constexpr int SEG = 32;
 
 struct SegArgs {
-  const uint32_t* key;
-  const uint32_t* pos;
+  const uint2* item;  // sorted (row, pair)
   const float* w;
   long long P, rows, out_ld, grad_ld;
   int R, vecs, tx_n, width;
@@ -564,14 +560,14 @@ __device__ __forceinline__ void get_part(const float* d, float (&x)[VEC]) {
 }
 
 // Whether `row` occurs in the sorted keys.
-__device__ __forceinline__ bool has_row(const uint32_t* __restrict__ key, long long P, uint32_t row) {
+__device__ __forceinline__ bool has_row(const uint2* __restrict__ item, long long P, uint32_t row) {
   long long lo = 0, hi = P;
   while (lo < hi) {
     const long long mid = (lo + hi) >> 1;
-    if (__ldg(key + mid) < row) lo = mid + 1;
+    if (__ldg(&item[mid].x) < row) lo = mid + 1;
     else hi = mid;
   }
-  return lo < P && __ldg(key + lo) == row;
+  return lo < P && __ldg(&item[lo].x) == row;
 }
 
 // ACC: added to d_table, whose rows are loaded with the pairs (SEG_U pairs in flight per team).
@@ -588,7 +584,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
     const long long w0 = (long long)(blockIdx.x - sum_blocks) * (LK_THREADS / 32) + (threadIdx.x >> 5);
     for (long long r0 = w0 * 32; r0 < a.rows; r0 += warps * 32) {
       const long long r = r0 + lane;
-      const bool zero = r < a.rows && !has_row(a.key, a.P, (uint32_t)r);
+      const bool zero = r < a.rows && !has_row(a.item, a.P, (uint32_t)r);
       unsigned todo = __ballot_sync(0xffffffffu, zero);
       while (todo) {
         const int l = __ffs(todo) - 1;
@@ -614,9 +610,9 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  uint32_t cur = a.key[p0];
-  const bool cut_start = p0 > 0 && a.key[p0 - 1] == cur;
-  const bool cut_end = p1 < a.P && a.key[p1] == a.key[p1 - 1];
+  uint32_t cur = a.item[p0].x;
+  const bool cut_start = p0 > 0 && a.item[p0 - 1].x == cur;
+  const bool cut_end = p1 < a.P && a.item[p1].x == a.item[p1 - 1].x;
   bool first = true;  // still in the range's first row
   GRow<G, VEC> last;  // (accumulate) the row of the pair before, if it was its row's last
   for (long long q0 = p0; q0 < p1; q0 += SEG_U) {
@@ -627,10 +623,11 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
 #pragma unroll
     for (int u = 0; u < SEG_U; ++u) {
       const long long p = q0 + u;
-      k[u] = p < p1 ? a.key[p] : none;
-      pr[u] = p < p1 ? a.pos[p] : 0u;
+      const uint2 x2 = p < p1 ? a.item[p] : make_uint2(none, 0u);
+      k[u] = x2.x;
+      pr[u] = x2.y;
     }
-    const uint32_t after = q0 + SEG_U < p1 ? a.key[q0 + SEG_U] : none;
+    const uint32_t after = q0 + SEG_U < p1 ? a.item[q0 + SEG_U].x : none;
     GRow<G, VEC> old[SEG_U];
 #pragma unroll
     for (int u = 0; u < SEG_U; ++u) {
@@ -688,14 +685,14 @@ lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
   const long long range = (long long)blockIdx.x * ty_n + ty;
   if (c >= a.vecs || range + 1 >= a.ranges) return;
   const long long p0 = range * SEG, p1 = p0 + SEG;  // not the last range: full
-  const uint32_t row = a.key[p1 - 1];
-  if (row == (uint32_t)a.rows || a.key[p1] != row) return;     // nothing cut at the end
-  if (a.key[p0] == row && p0 > 0 && a.key[p0 - 1] == row) return;  // the row began earlier
+  const uint32_t row = a.item[p1 - 1].x;
+  if (row == (uint32_t)a.rows || a.item[p1].x != row) return;     // nothing cut at the end
+  if (a.item[p0].x == row && p0 > 0 && a.item[p0 - 1].x == row) return;  // the row began earlier
   // last range that holds the row: the ranges after this one whose first key is the row
   long long lo = range + 1, hi = a.ranges;
   while (lo < hi) {
     const long long mid = (lo + hi) >> 1;
-    if (a.key[mid * SEG] == row) lo = mid + 1;
+    if (a.item[mid * SEG].x == row) lo = mid + 1;
     else hi = mid;
   }
   float acc[VEC];
@@ -742,7 +739,8 @@ SortPlan sort_plan(long long rows, long long P) {
 }
 
 struct BackWork {
-  uint32_t *key[2], *pos[2], *hist, *total;
+  uint2* item[2];
+  uint32_t *hist, *total;
   float* part;
 };
 size_t back_carve(const fwpkm_lookup_config& c, long long P, char* base, BackWork* w) {
@@ -756,8 +754,7 @@ size_t back_carve(const fwpkm_lookup_config& c, long long P, char* base, BackWor
   };
   BackWork b;
   for (int i = 0; i < 2; ++i) {
-    b.key[i] = (uint32_t*)take(4 * (size_t)P);
-    b.pos[i] = (uint32_t*)take(4 * (size_t)P);
+    b.item[i] = (uint2*)take(8 * (size_t)P);
   }
   b.hist = (uint32_t*)take(4 * (size_t)sp.tiles * sp.bins);
   b.total = (uint32_t*)take(4 * (size_t)sp.bins);
@@ -841,15 +838,50 @@ void launch_cluster(void (*kern)(KArgs...), unsigned grid, unsigned block, unsig
   cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// The sorted pairs end in w.key / w.pos [*sorted].  Up to CS_MAX pairs: one launch, which forms
+// Whether clusters of 16 CTAs of this kernel fit the current device (they are not portable).
+template <typename T, typename I, int VEC>
+bool wide_clusters() {
+  auto kern = sort_cluster_kernel<T, I, VEC>;
+  static std::atomic<int> known[64];  // by device: 0 not asked, 1 no, 2 yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  int k = known[dev].load();
+  if (k == 0) {
+    k = 1;
+    if (cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = CS_CLUSTER;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(CS_CLUSTER);
+      cfg.blockDim = dim3(CS_THREADS);
+      cfg.dynamicSmemBytes = CS_SMEM;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) k = 2;
+    }
+    cudaGetLastError();
+    known[dev].store(k);
+  }
+  return k == 2;
+}
+
+// The sorted pairs end in w.item[*sorted].  Up to CS_MAX pairs: one launch, which forms
 // dw too (dw.dw is cleared to say so).
 template <typename T, typename I, int VEC>
 int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const BackWork& w, int* sorted, DwArgs* dw,
             cudaStream_t s) {
   const SortPlan sp = sort_plan(c.rows, P);
   if (P <= CS_MAX) {
+    const void* kern = (const void*)sort_cluster_kernel<T, I, VEC>;
+    if (!raise_smem_limit(kern, CS_SMEM)) return -1;
+    // as many CTAs as there are thousands of pairs, up to the largest cluster that fits
     int ctas = 1;
-    while ((long long)ctas * CS_TILE < P) ctas <<= 1;
+    while (ctas < 8 && (long long)ctas * CS_THREADS < P) ctas <<= 1;
+    if (P > 8 * CS_THREADS && wide_clusters<T, I, VEC>()) ctas = 16;
+    const int items = (int)((P + (long long)ctas * CS_THREADS - 1) / ((long long)ctas * CS_THREADS));
     const int passes = (sp.bits + CS_BITS - 1) / CS_BITS, per = (sp.bits + passes - 1) / passes;
     long long more = 0;
     if (dw->dw) {
@@ -857,9 +889,8 @@ int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const Ba
       if (more > 148 - ctas) more = 148 - ctas;
       more = (more + ctas - 1) / ctas * ctas;
     }
-    if (!raise_smem_limit((const void*)sort_cluster_kernel<T, I, VEC>, CS_SMEM)) return -1;
     launch_cluster(sort_cluster_kernel<T, I, VEC>, (unsigned)(ctas + more), CS_THREADS, (unsigned)ctas, CS_SMEM, s,
-                   (const I*)idx, (int)P, c.rows, per, passes, ctas, w.key[0], w.pos[0], *dw);
+                   (const I*)idx, (int)P, c.rows, per, passes, ctas, items, w.item[0], *dw);
     dw->dw = nullptr;
     *sorted = 0;
     return 1;
@@ -870,7 +901,7 @@ int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const Ba
   int nl = 0;
   for (int pass = 0; pass < sp.passes; ++pass) {
     const int from = (pass + 1) & 1, to = pass & 1;
-    Source<I> src{(const I*)idx, pass ? w.key[from] : nullptr, pass ? w.pos[from] : nullptr, c.rows};
+    Source<I> src{(const I*)idx, pass ? w.item[from] : nullptr, c.rows};
     launch_k(sort_hist_kernel<I>, sp.tiles, RS_THREADS, 0, s, src, P, pass * sp.per, sp.bins, w.hist);
     ++nl;
     if (!own) {
@@ -878,7 +909,7 @@ int go_sort(const fwpkm_lookup_config& c, const void* idx, long long P, const Ba
       ++nl;
     }
     launch_k(sort_scatter_kernel<I>, sp.tiles, RS_THREADS, smem, s, src, P, pass * sp.per, sp.bins,
-             (const uint32_t*)w.hist, (const uint32_t*)w.total, sp.tiles, own, w.key[to], w.pos[to]);
+             (const uint32_t*)w.hist, (const uint32_t*)w.total, sp.tiles, own, w.item[to]);
     ++nl;
     *sorted = to;
   }
@@ -1048,8 +1079,7 @@ fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* t
     a.R = cfg->R; a.width = cfg->width; a.scale = cfg->scale; a.accumulate = accumulate != 0;
     a.ranges = (P + SEG - 1) / SEG;
     a.w = w;
-    a.key = bw.key[at];
-    a.pos = bw.pos[at];
+    a.item = bw.item[at];
     a.part = bw.part;
     if (bf)
       nl += grad_dtype == FWPKM_BF16 ? go_sum_v<__nv_bfloat16, __nv_bfloat16>(*cfg, a, d_out, d_table, s)
