@@ -18,6 +18,7 @@
 #include <cstdio>
 
 #include "fwpkm_internal.cuh"
+#include "sm100.cuh"
 
 namespace fwpkm {
 namespace {
@@ -494,6 +495,7 @@ sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, i
 // reads to SEG terms plus its partials.
 // ---------------------------------------------------------------------------
 constexpr int SEG = 32;
+constexpr int ZERO_ROWS = 8, ZERO_BYTES = 8192;
 
 struct SegArgs {
   const uint2* item;  // sorted (row, pair)
@@ -577,26 +579,41 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   pdl_wait();
   pdl_trigger();
   if ((int)blockIdx.x >= sum_blocks) {
-    // ---- rows no pair reads: zero (dense gradient only).  A warp takes 32 rows, each lane
-    // looks one of them up in the sorted keys, then the warp writes the missing ones.
+    // ---- rows no pair reads: zero (dense gradient only).  A warp takes ZERO_ROWS rows, a lane
+    // looks each of them up in the sorted keys, then the missing ones are written: by bulk
+    // copies of zeros from shared memory where rows are on the 16-byte grid
+    __shared__ __align__(16) uint8_t zeros[VEC == 1 ? 16 : ZERO_BYTES];
+    if (VEC > 1) {
+      for (int i = threadIdx.x * 16; i < ZERO_BYTES; i += LK_THREADS * 16)
+        *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0u, 0u, 0u, 0u);
+      sm100::fence_async_smem();
+      __syncthreads();
+    }
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)(gridDim.x - sum_blocks) * (LK_THREADS / 32);
     const long long w0 = (long long)(blockIdx.x - sum_blocks) * (LK_THREADS / 32) + (threadIdx.x >> 5);
-    for (long long r0 = w0 * 32; r0 < a.rows; r0 += warps * 32) {
+    for (long long r0 = w0 * ZERO_ROWS; r0 < a.rows; r0 += warps * ZERO_ROWS) {
       const long long r = r0 + lane;
-      const bool zero = r < a.rows && !has_row(a.item, a.P, (uint32_t)r);
-      unsigned todo = __ballot_sync(0xffffffffu, zero);
-      while (todo) {
-        const int l = __ffs(todo) - 1;
-        todo &= todo - 1;
-        G* dst = d_table + (r0 + l) * a.grad_ld;
-        constexpr int GV = VEC == 1 ? 1 : 16 / (int)sizeof(G);
-        Pack<G, GV> z;
-#pragma unroll
-        for (int e = 0; e < GV; ++e) z.v[e] = from_f<G>(0.f);
-        for (int c = lane; c < a.width / GV; c += 32) *reinterpret_cast<Pack<G, GV>*>(dst + (long long)c * GV) = z;
+      const bool zero = lane < ZERO_ROWS && r < a.rows && !has_row(a.item, a.P, (uint32_t)r);
+      if (VEC > 1) {
+        if (zero) {
+          const long long bytes = (long long)a.width * sizeof(G);
+          uint8_t* dst = (uint8_t*)(d_table + r * a.grad_ld);
+          for (long long o = 0; o < bytes; o += ZERO_BYTES)
+            sm100::bulk_store(dst + o, zeros, (uint32_t)(bytes - o < ZERO_BYTES ? bytes - o : ZERO_BYTES));
+          sm100::bulk_commit();
+        }
+      } else {
+        unsigned todo = __ballot_sync(0xffffffffu, zero);
+        while (todo) {
+          const int l = __ffs(todo) - 1;
+          todo &= todo - 1;
+          G* dst = d_table + (r0 + l) * a.grad_ld;
+          for (int c = lane; c < a.width; c += 32) dst[c] = from_f<G>(0.f);
+        }
       }
     }
+    if (VEC > 1) sm100::bulk_wait_all();
     return;
   }
   const int ty_n = LK_THREADS / a.tx_n;
@@ -923,12 +940,12 @@ int go_sum(const fwpkm_lookup_config& c, SegArgs a, const void* d_out, void* d_t
   const int ty = LK_THREADS / a.tx_n;
   const unsigned gy = (unsigned)((a.vecs + a.tx_n - 1) / a.tx_n);
   const unsigned sb = (unsigned)((a.ranges + ty - 1) / ty);
-  // dense gradient: CTAs that zero the rows nothing reads, up to four per SM, each at least
-  // 8 warps x 32 rows (column blocks share one row split: only blockIdx.y == 0 has them)
+  // dense gradient: CTAs that zero the rows nothing reads, 64 rows each (up to 16 per SM's
+  // place, then more; column blocks share one row split: only blockIdx.y == 0 has them)
   long long zb = 0;
   if (!ACC) {
-    zb = (a.rows + 255) / 256;
-    if (zb > 148 * 4) zb = 148 * 4;
+    zb = (a.rows + 63) / 64;
+    if (zb > 148 * 32) zb = 148 * 32;
   }
   if (sb + zb == 0) return 0;
   int nl = 0;
