@@ -92,27 +92,28 @@ __device__ __forceinline__ float team_reduce(float x, float* red) {
   return x;
 }
 
-// v -> softmax(v) over the team; false (v = 0) for a row without a finite logit.  The maximum
-// passes NaN by, but the sum keeps it.
+// v -> exp(v - max) over the team; returns 1 / their sum, 0 (v = 0) for a row without a finite
+// logit.  The maximum passes NaN by, but the sum keeps it.  exp is 2^(v log2 e - max log2 e),
+// one FMA and the hardware's 2^x (2^-22 relative; the FMA's rounding is that of v - max, and
+// that of max log2 e is common to the row): with expf, 32 values a lane, the instructions and
+// not the loads bounded both directions.
 template <int NV, int L>
-__device__ __forceinline__ bool team_softmax(float (&v)[NV], float* red) {
+__device__ __forceinline__ float team_exp(float (&v)[NV], float* red) {
+  constexpr float LOG2E = 1.4426950408889634f;
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
   m = team_reduce<L, true>(m, red);
-  float s = 0.f;
   const bool none = m == -INFINITY;
+  const float shift = none ? 0.f : -m * LOG2E;
+  float s = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    v[i] = none && !isnan(v[i]) ? 0.f : expf(v[i] - m);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(fmaf(v[i], LOG2E, shift)));
     s += v[i];
   }
   s = team_reduce<L, false>(s, red);
-  if (s == 0.f) return false;
-  const float inv = 1.f / s;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] *= inv;
-  return true;
+  return s == 0.f ? 0.f : 1.f / s;
 }
 
 template <typename T, int VEC, int NCH, int L>
@@ -148,9 +149,10 @@ balance_sum_kernel(BalArgs a) {
     float v[NV];
     take_row<T, VEC, NCH, L>(next, next_on, a.E, l, v);
     next_on = fetch_row<T, VEC, NCH, L>(x, mask, tb + TEAMS + team, t1, a.ld, a.E, l, next);
-    if (team_softmax<NV, L>(v, red)) {
+    const float inv = team_exp<NV, L>(v, red);
+    if (inv != 0.f) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += v[i];
+      for (int i = 0; i < NV; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
       n += l == 0;
     }
   }
@@ -314,11 +316,12 @@ balance_grad_kernel(BalArgs a, const float* __restrict__ slope, const float* __r
     float v[NV];
     take_row<T, VEC, NCH, L>(next, next_on, a.E, l, v);
     next_on = fetch_row<T, VEC, NCH, L>(x, mask, t + step, a.T, a.ld, a.E, l, next);
-    const bool live = team_softmax<NV, L>(v, red);
+    const float inv = team_exp<NV, L>(v, red);
     float c = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) c = fmaf(v[i], s[i], c);
-    c = team_reduce<L, false>(c, red);
+    c = team_reduce<L, false>(c, red) * inv;
+    const float f = gl * inv;
     if (in) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
@@ -327,7 +330,7 @@ balance_grad_kernel(BalArgs a, const float* __restrict__ slope, const float* __r
           BPack<T, VEC> p;
 #pragma unroll
           for (int u = 0; u < VEC; ++u)
-            bal_put(p.v[u], live ? gl * v[j * VEC + u] * (s[j * VEC + u] - c) : 0.f);
+            bal_put(p.v[u], inv != 0.f ? f * v[j * VEC + u] * (s[j * VEC + u] - c) : 0.f);
           *reinterpret_cast<BPack<T, VEC>*>(d + t * a.E + e) = p;
         }
       }
