@@ -18,6 +18,7 @@
 // registers (one read), column sums in registers over the team's rows, joined over the
 // CTA's teams in team order; a second launch joins the CTAs' partial sums in order, in fp64.
 // No float atomics, so the results are deterministic; the counts are integer sums.
+#include <cmath>
 #include <cstdio>
 
 #include "fwpkm_internal.cuh"
@@ -196,7 +197,7 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
 // `sl` threads share a column when there are fewer columns than threads: slice i adds CTAs
 // i, i + sl, ..; the slices are added in order.
 __global__ void __launch_bounds__(BL_JOIN)
-balance_join_kernel(BalArgs a, int sl, int kind, float coef, float* __restrict__ loss, int32_t* __restrict__ counts,
+balance_join_kernel(BalArgs a, int sl, int kind, float coef, double log_e, float* __restrict__ loss, int32_t* __restrict__ counts,
                     float* __restrict__ usage, float* __restrict__ slope) {
   __shared__ double red[BL_JOIN / 32];
   __shared__ double su[BL_JOIN];
@@ -221,17 +222,17 @@ balance_join_kernel(BalArgs a, int sl, int kind, float coef, float* __restrict__
     if (e < a.E && (i == 0 || sl == 1)) {
       const float* part = a.part + (long long)g * a.ctas * a.E + e;
       const int32_t* cp = a.cpart + (long long)g * a.ctas * a.E + e;
-      for (int q = slice; q < a.ctas; q += 8 * sl) {
-        float f[8];
-        int k[8];
+      for (int q = slice; q < a.ctas; q += 16 * sl) {
+        float f[16];
+        int k[16];
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
+        for (int v = 0; v < 16; ++v) {
           const bool in = q + v * sl < a.ctas;
           f[v] = in ? part[(long long)(q + v * sl) * a.E] : 0.f;
           k[v] = in && a.idx ? cp[(long long)(q + v * sl) * a.E] : 0;
         }
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
+        for (int v = 0; v < 16; ++v) {
           s += f[v];
           c += k[v];
         }
@@ -271,9 +272,8 @@ balance_join_kernel(BalArgs a, int sl, int kind, float coef, float* __restrict__
         l += a.E * f * ue;
         ae = csum > 0.0 ? a.E * f - 1.0 : 0.0;
       } else {
-        const double lg = ue > 0.0 ? log(ue) : (ue == 0.0 ? 0.0 : ue);  // NaN stays
-        l += ue * lg;
-        ae = ue > 0.0 ? lg + log((double)a.E) : (ue == 0.0 ? 0.0 : ue);
+        ae = ue > 0.0 ? log(ue * a.E) : (ue == 0.0 ? 0.0 : ue);  // NaN stays
+        l += ue * (ae - log_e);
       }
       const long long o = (long long)g * a.E + e;
       usage[o] = (float)ue;
@@ -494,7 +494,8 @@ fwpkm_status fwpkm_balance_loss(const fwpkm_balance_config* cfg, const void* x, 
   if (!ok) return FWPKM_ERR_CUDA;
   int sl = 1;
   while (sl < 32 && (long long)sl * 2 * cfg->experts <= BL_JOIN && sl < r.a.ctas) sl <<= 1;
-  launch_k(balance_join_kernel, cfg->groups, BL_JOIN, 0, r.s, r.a, sl, cfg->kind, cfg->coef, loss, counts, usage,
+  launch_k(balance_join_kernel, cfg->groups, BL_JOIN, 0, r.s, r.a, sl, cfg->kind, cfg->coef, log((double)cfg->experts),
+           loss, counts, usage,
            slope);
   return bal_done(2);
 }
