@@ -242,7 +242,7 @@ scan_kernel(ScanArgs a, int lj, int tb, int local) {
 // not compound over thousands of tokens.  (The batched pass needed 1146 instructions a warp for
 // one token and was bound by them: 61 us for 2048 heads of 128 x 128, 42 at the copy bandwidth.)
 template <typename T, int NI>
-__global__ void __launch_bounds__(SC_THREADS)
+__global__ void __launch_bounds__(SC_THREADS, 4)
 step_kernel(ScanArgs a, int lj) {
   __shared__ __align__(16) float sr[2][SC_WARPS][128];
   __shared__ float sa[2];
