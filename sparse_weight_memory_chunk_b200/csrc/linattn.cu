@@ -15,23 +15,30 @@
 //
 // The CUDA-core pass keeps S in fp32 registers: a CTA of 256 threads owns up to 128 columns
 // of one head's state, thread (row group, column quad) NI x 4 of its elements, and takes the
-// tokens of a batch in order: 2 FMA per state element and token.  Inside a batch of SC_TB
-// tokens the state is kept relative to the batch's start (k_u enters as a^-u k_u, o_u leaves
-// as a^u o_u), so the decay costs one multiplication per batch and its rounding does not
-// compound over the tokens; a head whose a^-SC_TB would leave fp32's range decays token by
-// token.  Bound: for single tokens the state's bytes (read and written once); for prompts
-// the FMAs.
+// tokens of a batch in order: 2 FMA per state element and token.  The next batch's rows come by
+// asynchronous copies meanwhile.  Inside a batch of SC_TB tokens the state is kept relative to
+// the batch's start (v_u enters as a^-u v_u, o_u leaves as a^u o_u), so the decay costs one
+// multiplication per batch and its rounding does not compound over the tokens; a head whose
+// a^-SC_TB would leave fp32's range takes batches of one token.  Bound: instruction issue
+// (194 a warp and token at d = d_v = 128, of them 64 packed FMAs): 256 heads of 512 tokens in
+// 350 us, 49 TFLOP/s.  (With rows staged by plain loads between two barriers the loads'
+// latency bounded it: 128 such heads in 665 us, now 232.)
 #include <cstdio>
 
 #include "linattn.cuh"
+#include "sm100.cuh"
 
 namespace fwpkm {
 namespace {
 
 constexpr int SC_THREADS = 256;
 constexpr int SC_WARPS = SC_THREADS / 32;
-constexpr int SC_TB = 16;        // tokens per batch
+constexpr int SC_TB = 8;         // tokens per batch
+constexpr int SC_STEP = 16;      // tokens that the kernel for a few of them takes at most
 constexpr int SC_MAX_D = 256;    // rows of the state at most
+constexpr int SC_SEGS = 2 * 148; // CTAs that the GPU holds at once, and segments of a pass at most
+constexpr int SC_SPLIT = 256;    // tokens from which a prompt is split
+constexpr int SC_SEG_MIN = 64;   // tokens per segment at least
 constexpr float SC_RANGE = 40.f; // largest |log a^SC_TB| kept relative to the batch
 
 __device__ __forceinline__ float sc_f(float x) { return x; }
@@ -44,19 +51,87 @@ __device__ __forceinline__ const T* head_row(const fwpkm_heads& x, int b, int h)
   return (const T*)x.p + (long long)b * x.sb + (long long)h * x.sh;
 }
 
-// local: the segment's own state from zero into its slot, no output.
+// One row of `bytes` bytes into shared memory by a warp, in units of 16 or 4 bytes without waiting
+// (both ends on that grid; a last unit may be shorter), or of 2 bytes where a row of bf16 is on no
+// such grid.
+__device__ __forceinline__ void copy_row(uint32_t dst, const char* src, int bytes, int unit, int lane) {
+  if (unit == 16) {
+    for (int o = lane * 16; o < bytes; o += 512)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + o), "l"(src + o), "r"(min(16, bytes - o))
+                   : "memory");
+  } else if (unit == 4) {
+    for (int o = lane * 4; o < bytes; o += 128)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + o), "l"(src + o), "r"(min(4, bytes - o))
+                   : "memory");
+  } else {
+    unsigned short x[SC_MAX_D / 32];
+#pragma unroll
+    for (int i = 0; i < SC_MAX_D / 32; ++i) {
+      const int o = (i * 32 + lane) * 2;
+      x[i] = o < bytes ? __ldg(reinterpret_cast<const unsigned short*>(src + o)) : (unsigned short)0;
+    }
+#pragma unroll
+    for (int i = 0; i < SC_MAX_D / 32; ++i) {
+      const int o = (i * 32 + lane) * 2;
+      if (o < bytes) asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + o), "h"(x[i]) : "memory");
+    }
+  }
+}
+
+// N values in a row of shared memory (N * sizeof(T) a multiple of 16, or N <= 4).
+template <int N>
+__device__ __forceinline__ void get_row(const float* p, float (&x)[N]) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p + i);
+      x[i] = y.x; x[(i + 1) % N] = y.y; x[(i + 2) % N] = y.z; x[(i + 3) % N] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = p[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void get_row(const __nv_bfloat16* p, float (&x)[N]) {
+  if (N % 4 == 0) {
+    constexpr int V = N % 8 == 0 ? 4 : 2;  // words per load
+#pragma unroll
+    for (int i = 0; i < N; i += 2 * V) {
+      uint32_t w[4];
+      if (V == 4) {
+        const uint4 y = *reinterpret_cast<const uint4*>(p + i);
+        w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
+      } else {
+        const uint2 y = *reinterpret_cast<const uint2*>(p + i);
+        w[0] = y.x; w[1] = y.y;
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x[(i + 2 * j) % N] = __uint_as_float(w[j] << 16);
+        x[(i + 2 * j + 1) % N] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __bfloat162float(p[i]);
+  }
+}
+
+// local: the segment's own state from zero into its slot, no output.  unit: bytes per copy of
+// the rows of q, k and v.
 template <typename T, int NI>
-__global__ void __launch_bounds__(SC_THREADS)
-scan_kernel(ScanArgs a, int lj, int tb, int local) {
-  extern __shared__ float sm[];
+__global__ void __launch_bounds__(SC_THREADS, 2)
+scan_kernel(ScanArgs a, int lj, int unit, int local) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ float s_in[SC_TB], s_out[SC_TB];        // a^-u and a^u
   pdl_wait();
   pdl_trigger();
   const int rgn = SC_THREADS / lj, dp = rgn * NI;   // row groups, padded d
   const int cols = 4 * lj, tiles = (a.dv + cols - 1) / cols;
-  float* sk = sm;                                    // [tb][dp]
-  float* sq = sk + tb * dp;                          // [tb][dp]
-  float* sv = sq + tb * dp;                          // [tb][cols]
-  float* sr = sv + tb * cols;                        // [tb][SC_WARPS][cols] partial outputs
+  const int row = 2 * dp + cols;                     // k, q and v of a token
+  float* sr = sm;                                    // [SC_TB][SC_WARPS][cols] partial outputs
+  T* raw = reinterpret_cast<T*>(sr + SC_TB * SC_WARPS * cols);  // [2][SC_TB][row]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int jl = tid & (lj - 1), rg = tid / lj;
   const long long bh = blockIdx.x / tiles;
@@ -67,8 +142,35 @@ scan_kernel(ScanArgs a, int lj, int tb, int local) {
   const int n = scan_len(a, b);
   const int t0 = min(n, g * a.seg_len), t1 = min(n, t0 + a.seg_len);
   const float ld = a.log_decay[h];
-  const bool fast = fabsf(ld) * (float)SC_TB <= SC_RANGE;
+  // tokens per batch: one where a^-SC_TB would leave fp32's range
+  const int tb = fabsf(ld) * (float)SC_TB <= SC_RANGE ? SC_TB : 1;
   const size_t cells = (size_t)a.d * a.dv;
+
+  const T* qp = head_row<T>(a.q, b, h);
+  const T* kp = head_row<T>(a.k, b, h);
+  const T* vp = head_row<T>(a.v, b, h) + c0;
+  static_assert(SC_TB == SC_WARPS, "a warp copies one token of a batch");
+  // a batch's rows on their way: warp u takes token u
+  auto fetch = [&](int tb0, int buf) {
+    if (warp < min(tb, t1 - tb0)) {
+      const long long t = a.reverse ? n - 1 - (tb0 + warp) : tb0 + warp;
+      const uint32_t dst = sm100::smem_u32(raw + (buf * SC_TB + warp) * row);
+      copy_row(dst, (const char*)(kp + t * a.k.st), a.d * (int)sizeof(T), unit, lane);
+      if (!local) copy_row(dst + dp * (int)sizeof(T), (const char*)(qp + t * a.q.st), a.d * (int)sizeof(T), unit, lane);
+      copy_row(dst + 2 * dp * (int)sizeof(T), (const char*)(vp + t * a.v.st), min(cols, a.dv - c0) * (int)sizeof(T), unit,
+               lane);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // the padding of a row is zero throughout
+  for (int x = tid * 16; x < 2 * SC_TB * row * (int)sizeof(T); x += SC_THREADS * 16)
+    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(raw) + x) = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < SC_TB) {
+    s_in[tid] = decay_pow(-ld, (float)tid);   // (a batch of one token reads the first only)
+    s_out[tid] = decay_pow(ld, (float)tid) * a.out_scale;
+  }
+  __syncthreads();
+  fetch(t0, 0);
 
   // start state, decayed for the first token
   float S[NI][4];
@@ -110,104 +212,73 @@ scan_kernel(ScanArgs a, int lj, int tb, int local) {
     }
   }
 
-  const T* qp = head_row<T>(a.q, b, h);
-  const T* kp = head_row<T>(a.k, b, h);
-  const T* vp = head_row<T>(a.v, b, h);
-  T* op = (T*)a.o.p + (long long)b * a.o.sb + (long long)h * a.o.sh;
+  T* op = (T*)a.o.p + (long long)b * a.o.sb + (long long)h * a.o.sh + c0;
   const float a1 = decay_pow(ld, 1.f);
-  for (int tb0 = t0; tb0 < t1; tb0 += tb) {
+  // a^tb in two parts
+  float whole, rest;
+  {
+    const double w = exp((double)ld * tb);
+    whole = (float)w;
+    rest = (float)(w - (double)whole);
+  }
+  int buf = 0;
+  for (int tb0 = t0; tb0 < t1; tb0 += tb, buf ^= 1) {
     const int m = min(tb, t1 - tb0);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    for (int x = tid; x < m * dp; x += SC_THREADS) {
-      const int u = x / dp, i = x - u * dp;
-      const long long t = a.reverse ? n - 1 - (tb0 + u) : tb0 + u;
-      float kv = 0.f, qv = 0.f;
-      if (i < a.d) {
-        kv = sc_f(kp[t * a.k.st + i]);
-        if (fast) kv *= decay_pow(-ld, (float)u);
-        if (!local) qv = sc_f(qp[t * a.q.st + i]);
-      }
-      sk[x] = kv;
-      if (!local) sq[x] = qv;
-    }
-    for (int x = tid; x < m * cols; x += SC_THREADS) {
-      const int u = x / cols, j = x - u * cols;
-      const long long t = a.reverse ? n - 1 - (tb0 + u) : tb0 + u;
-      sv[x] = c0 + j < a.dv ? sc_f(vp[t * a.v.st + c0 + j]) : 0.f;
-    }
-    __syncthreads();
+    if (tb0 + tb < t1) fetch(tb0 + tb, buf ^ 1);
     const bool last = tb0 + m >= t1;
-    for (int u = 0; u < m; ++u) {
-      const float4 v4 = *reinterpret_cast<const float4*>(sv + u * cols + 4 * jl);
-      float o[4] = {0.f, 0.f, 0.f, 0.f};
-      float kk[NI], qq[NI];
-      if (NI % 4 == 0) {
+    const T* rows = raw + buf * SC_TB * row;
+#pragma unroll 1
+    for (int u = 0; u < m; ++u, rows += row) {
+      float x[NI], v[4];
+      get_row<NI>(rows + i0, x);
+      get_row<4>(rows + 2 * dp + 4 * jl, v);
+      const float w = s_in[u];
 #pragma unroll
-        for (int i = 0; i < NI; i += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(sk + u * dp + i0 + i);
-          kk[i] = x.x; kk[(i + 1) % NI] = x.y; kk[(i + 2) % NI] = x.z; kk[(i + 3) % NI] = x.w;
-        }
-      } else {
+      for (int e = 0; e < 4; ++e) v[e] *= w;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) kk[i] = sk[u * dp + i0 + i];
-      }
+      for (int i = 0; i < NI; i += 2)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        S[i][0] = fmaf(kk[i], v4.x, S[i][0]);
-        S[i][1] = fmaf(kk[i], v4.y, S[i][1]);
-        S[i][2] = fmaf(kk[i], v4.z, S[i][2]);
-        S[i][3] = fmaf(kk[i], v4.w, S[i][3]);
-      }
+        for (int e = 0; e < 4; ++e) sm100::fma2(S[i][e], S[i + 1][e], x[i], x[i + 1], v[e], v[e]);
       if (!local) {
-        if (NI % 4 == 0) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, o1[4] = {0.f, 0.f, 0.f, 0.f};  // even and odd rows
+        get_row<NI>(rows + dp + i0, x);
 #pragma unroll
-          for (int i = 0; i < NI; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(sq + u * dp + i0 + i);
-            qq[i] = x.x; qq[(i + 1) % NI] = x.y; qq[(i + 2) % NI] = x.z; qq[(i + 3) % NI] = x.w;
-          }
-        } else {
+        for (int i = 0; i < NI; i += 2)
 #pragma unroll
-          for (int i = 0; i < NI; ++i) qq[i] = sq[u * dp + i0 + i];
-        }
+          for (int e = 0; e < 4; ++e) sm100::fma2(o[e], o1[e], x[i], x[i + 1], S[i][e], S[i + 1][e]);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = fmaf(qq[i], S[i][e], o[e]);
+        for (int e = 0; e < 4; ++e) o[e] += o1[e];
         for (int off = lj; off < 32; off <<= 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], off);
         if (lane < lj)
           *reinterpret_cast<float4*>(sr + (u * SC_WARPS + warp) * cols + 4 * jl) = make_float4(o[0], o[1], o[2], o[3]);
       }
-      // token by token: decay for the next one (not after the segment's last)
-      if (!fast && !(last && u == m - 1)) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[i][e] *= a1;
-      }
     }
-    if (fast) {
-      // back to absolute: a^m for the next batch's first token, a^(m-1) after the last token
-      const float e = (float)(last ? m - 1 : m);
-      const double w = exp((double)ld * e);
-      const float hi = (float)w, lo = (float)(w - (double)hi);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) S[i][x] = fmaf(S[i][x], hi, S[i][x] * lo);
+    // back to absolute: a^tb for the next batch's first token, a^(m-1) after the last token
+    float hi = whole, lo = rest;
+    if (last) {
+      const double w = m == 1 ? 1.0 : exp((double)ld * (m - 1));
+      hi = (float)w;
+      lo = (float)(w - (double)hi);
     }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) S[i][x] = fmaf(S[i][x], hi, S[i][x] * lo);
     if (!local) {
       __syncthreads();
-      for (int x = tid; x < m * cols; x += SC_THREADS) {
-        const int u = x / cols, j = x - u * cols;
-        if (c0 + j < a.dv) {
-          float s = 0.f;
+      // warp u writes token u
+      if (warp < m) {
+        const long long t = a.reverse ? n - 1 - (tb0 + warp) : tb0 + warp;
+        const float f = s_out[warp];
+        for (int j = lane; j < cols && c0 + j < a.dv; j += 32) {
+          float x = 0.f;
 #pragma unroll
-          for (int w = 0; w < SC_WARPS; ++w) s += sr[(u * SC_WARPS + w) * cols + j];
-          const long long t = a.reverse ? n - 1 - (tb0 + u) : tb0 + u;
-          if (fast) s *= decay_pow(ld, (float)u);
-          sc_put(op + t * a.o.st + c0 + j, s * a.out_scale);
+          for (int w = 0; w < SC_WARPS; ++w) x += sr[(warp * SC_WARPS + w) * cols + j];
+          sc_put(op + t * a.o.st + j, x * f);
         }
       }
     }
@@ -323,13 +394,22 @@ __global__ void __launch_bounds__(256)
 scan_combine_kernel(ScanArgs a) {
   pdl_wait();
   pdl_trigger();
+  __shared__ float2 decay[SC_SEGS];  // a^len of every segment, in two parts
   const size_t cells = (size_t)a.d * a.dv;
   const size_t x = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (x >= cells) return;
   const long long bh = blockIdx.y;
   const int b = (int)(bh / a.H), h = (int)(bh - (long long)b * a.H);
   const int n = scan_len(a, b);
   const float ld = a.log_decay[h];
+  for (int g = threadIdx.x; g < a.nseg - 1; g += 256) {
+    const int len = max(0, min(n - g * a.seg_len, a.seg_len));
+    const int e = len - (g == 0 && a.in_ready && len > 0 ? 1 : 0);
+    const double w = e == 0 ? 1.0 : exp((double)ld * e);
+    decay[g].x = (float)w;
+    decay[g].y = (float)(w - (double)decay[g].x);
+  }
+  __syncthreads();
+  if (x >= cells) return;
   const int i = (int)(x / a.dv), j = (int)(x - (size_t)i * a.dv);
   float* slot = a.slots + (size_t)bh * a.nseg * cells + x;
   float E = a.s_in ? a.s_in[(size_t)bh * cells + i * a.si + j * a.sj] * (n == 0 ? 1.f : a.in_scale) : 0.f;
@@ -342,11 +422,8 @@ scan_combine_kernel(ScanArgs a) {
     for (int u = 0; u < 8; ++u) {
       const int g = g0 + u;
       if (g >= a.nseg - 1) break;
-      const int len = max(0, min(n - g * a.seg_len, a.seg_len));
-      const int e = len - (g == 0 && a.in_ready && len > 0 ? 1 : 0);
-      const double w = e == 0 ? 1.0 : exp((double)ld * e);
-      const float hi = (float)w, lo = (float)(w - (double)hi);
-      E = fmaf(E, hi, fmaf(E, lo, loc[u]));
+      const float2 w = decay[g];
+      E = fmaf(E, w.x, fmaf(E, w.y, loc[u]));
       slot[(size_t)g * cells] = E;
     }
   }
@@ -362,18 +439,29 @@ int pow2_ceil(int x) {
 struct ScanShape {
   int lj, ni, tiles;
 };
-// Column quads per CTA: as wide as 16 rows per thread allow; narrower tiles when the heads
-// alone do not fill the GPU and the tokens are too few to split (each tile re-reads q and k).
+// Column quads per CTA: as wide as 16 rows per thread allow.  Narrower tiles (each re-reads q and
+// k) where the heads and the segments that T allows leave half of the GPU's places empty and
+// narrower ones fill them: 10 heads of 72 x 100 with 1003 tokens 91 -> 65 us, 8 of 128 x 128 with
+// 100 tokens 51 -> 35; but with four rows a thread or fewer a token costs its latency, not its
+// work, so there only a quarter counts (128 heads of 64 x 64, 512 tokens: 147 us wide, 172 narrow).
 ScanShape scan_shape(const ScanArgs& a) {
   int lj = SC_THREADS * 16 / (pow2_ceil(a.d) < 16 ? 16 : pow2_ceil(a.d));
   if (lj > 32) lj = 32;
   const int need = pow2_ceil((a.dv + 3) / 4);
   if (lj > need) lj = need < 4 ? 4 : need;
-  if (a.T <= 64)
-    while (lj > 4 && (long long)a.B * a.H * ((a.dv + 4 * lj - 1) / (4 * lj)) < 148) lj >>= 1;
-  const int rg = SC_THREADS / lj;
-  int ni = 1;
-  while (ni * rg < a.d) ni <<= 1;
+  auto ctas = [&](int l) {  // with as many segments as fit
+    const long long base = (long long)a.B * a.H * ((a.dv + 4 * l - 1) / (4 * l));
+    long long n = a.T < SC_SPLIT || base > SC_SEGS / 3 ? 1 : SC_SEGS / base;
+    if (n > a.T / SC_SEG_MIN) n = a.T / SC_SEG_MIN;
+    return base * (n < 1 ? 1 : n);
+  };
+  auto rows = [&](int l) {
+    int ni = 2;
+    while (ni * (SC_THREADS / l) < a.d) ni <<= 1;
+    return ni;
+  };
+  while (lj > 4 && ctas(lj) <= (rows(lj) > 4 ? 150 : 75) && 2 * ctas(lj / 2) >= 3 * ctas(lj)) lj >>= 1;
+  const int ni = rows(lj);
   return {lj, ni, (a.dv + 4 * lj - 1) / (4 * lj)};
 }
 
@@ -381,27 +469,36 @@ ScanShape scan_shape(const ScanArgs& a) {
 // about two CTAs per SM, of at least 64 tokens each.
 int scan_segments(const ScanArgs& a) {
   const long long base = (long long)a.B * a.H * scan_shape(a).tiles;
-  if (base >= 148 || a.T < 256) return 1;
-  long long n = (2 * 148 + base - 1) / base;
-  const long long most = a.T / 64;
+  if (base > SC_SEGS / 3 || a.T < SC_SPLIT) return 1;
+  long long n = SC_SEGS / base;
+  const long long most = a.T / SC_SEG_MIN;
   if (n > most) n = most;
   return n < 2 ? 1 : (int)n;
+}
+
+// Bytes per asynchronous copy: the largest grid that every row starts on.
+template <typename T>
+int copy_unit(const ScanArgs& a, int cols) {
+  const int es = (int)sizeof(T);
+  unsigned long long bits = (unsigned long long)cols * es;
+  for (const fwpkm_heads* x : {&a.q, &a.k, &a.v})
+    bits |= (unsigned long long)(uintptr_t)x->p | (unsigned long long)((x->sb | x->sh | x->st) * es);
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
 }
 
 template <typename T>
 int go_scan(const ScanArgs& a, int local, cudaStream_t s) {
   const ScanShape sh = scan_shape(a);
-  const int tb = a.T < SC_TB ? (a.T < 1 ? 1 : a.T) : SC_TB;
   const int rg = SC_THREADS / sh.lj, dp = rg * sh.ni, cols = 4 * sh.lj;
-  const size_t smem = 4 * (size_t)tb * (2 * dp + cols + SC_WARPS * cols);
+  const size_t smem = SC_TB * ((size_t)4 * SC_WARPS * cols + 2 * sizeof(T) * (2 * dp + cols));
+  const int unit = copy_unit<T>(a, cols);
   const dim3 grid((unsigned)((long long)a.B * a.H * sh.tiles), local ? a.nseg - 1 : a.nseg);
 #define FWPKM_SCAN(NI)                                                                           \
   case NI:                                                                                       \
     if (smem > 48 * 1024 && !raise_smem_limit((const void*)scan_kernel<T, NI>, smem)) return -1; \
-    launch_k(scan_kernel<T, NI>, grid, SC_THREADS, smem, s, a, sh.lj, tb, local);                 \
+    launch_k(scan_kernel<T, NI>, grid, SC_THREADS, smem, s, a, sh.lj, unit, local);               \
     break;
   switch (sh.ni) {
-    FWPKM_SCAN(1)
     FWPKM_SCAN(2)
     FWPKM_SCAN(4)
     FWPKM_SCAN(8)
@@ -414,7 +511,7 @@ int go_scan(const ScanArgs& a, int local, cudaStream_t s) {
 
 // Whether the kernel for a few tokens takes this pass (states in whole 16-byte vectors).
 bool step_takes(const ScanArgs& a) {
-  return a.T <= SC_TB && a.dv % 4 == 0 && a.s_in && a.s_out && la_al(a.s_in, 16) && la_al(a.s_out, 16);
+  return a.T <= SC_STEP && a.dv % 4 == 0 && a.s_in && a.s_out && la_al(a.s_in, 16) && la_al(a.s_out, 16);
 }
 int launch_step(const ScanArgs& a, int dtype, cudaStream_t s) {
   // eight rows of the state per thread; narrower column tiles when the heads do not fill the GPU

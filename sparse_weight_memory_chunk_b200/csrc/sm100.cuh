@@ -144,6 +144,13 @@ __device__ __forceinline__ void sub2(float& x, float& y, float u, float v) {
       : "+f"(x), "+f"(y)
       : "f"(u), "f"(v));
 }
+// x += a c, y += b d
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mov.b64 r, {%4, %5};\n"
+      " fma.rn.f32x2 p, q, r, p;\n mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
 // x = x f + u, y = y f + v
 __device__ __forceinline__ void fma2(float& x, float& y, float f, float u, float v) {
   asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 c, {%3, %4};\n fma.rn.f32x2 a, a, "
