@@ -16,7 +16,7 @@
 // Bytes: x read once per direction, dx written once; ~8 operations per logit: bound by HBM.
 // Forward: CTAs over blocks of a group's rows, a team of lanes per row with the row in
 // registers (one read), column sums in registers over the team's rows, joined over the
-// CTA's teams in team order; a second launch joins the CTAs' partial sums in order, in fp64.
+// CTA's teams in team order; a second launch joins the CTAs' partial sums in a fixed order, in fp64.
 // No float atomics, so the results are deterministic; the counts are integer sums.
 #include <cmath>
 #include <cstdio>
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int BL_THREADS = 256;
 constexpr int BL_MAX_E = 4096;
-constexpr int BL_JOIN = 1024;
+constexpr int BL_JOIN = 512;
 
 struct BalArgs {
   const void* x;
@@ -40,6 +40,9 @@ struct BalArgs {
   float* part;             // [G][ctas][E] partial usage sums
   int32_t* cpart;          // [G][ctas][E] partial counts
   int32_t* npart;          // [G][ctas] rows with a softmax
+  double* usum;            // [G][E] their sums over the CTAs
+  int32_t* csum;           // [G][E]
+  int* done;               // [G] CTAs of the join that have written theirs
 };
 
 template <typename T, int VEC>
@@ -177,7 +180,10 @@ balance_sum_kernel(BalArgs a) {
     part[e] = s;
     if (a.idx) a.cpart[((long long)g * a.ctas + cta) * a.E + e] = cnt[e];
   }
-  if (threadIdx.x == 0) a.npart[(long long)g * a.ctas + cta] = s_n;
+  if (threadIdx.x == 0) {
+    a.npart[(long long)g * a.ctas + cta] = s_n;
+    if (cta == 0) a.done[g] = 0;
+  }
 }
 
 __device__ __forceinline__ double block_sum(double x, double* red) {
@@ -186,85 +192,95 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
-  static_assert(BL_JOIN == 1024, "one value per lane");
-  x = red[threadIdx.x & 31];
+  x = (threadIdx.x & 31) < BL_JOIN / 32 ? red[threadIdx.x & 31] : 0.0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// One CTA per group: the CTAs' partial sums in CTA order -> usage, counts, loss, slope.
-// `sl` threads share a column when there are fewer columns than threads: slice i adds CTAs
-// i, i + sl, ..; the slices are added in order.
+// The CTAs' partial sums -> usage, counts, loss, slope.  A CTA takes BL_JOIN / slices columns of a
+// group: slice i of its threads adds CTAs i, i + slices, .. and the slices are added in order.  The
+// group's last CTA to finish has all columns' sums before it and forms the results.  (By one
+// CTA per group the chain of loads took 30 us for 2 groups of 256 experts from 295 CTAs each,
+// and by a cluster of eight 58 us for one of 4096.)
 __global__ void __launch_bounds__(BL_JOIN)
-balance_join_kernel(BalArgs a, int sl, int kind, float coef, double log_e, float* __restrict__ loss, int32_t* __restrict__ counts,
+balance_join_kernel(BalArgs a, int slices, int kind, float coef, double log_e, float* __restrict__ loss, int32_t* __restrict__ counts,
                     float* __restrict__ usage, float* __restrict__ slope) {
   __shared__ double red[BL_JOIN / 32];
   __shared__ double su[BL_JOIN];
   __shared__ int sc[BL_JOIN];
+  __shared__ int s_last;
   pdl_wait();
   pdl_trigger();
-  const int g = blockIdx.x;
-  const int cols = BL_JOIN / sl;                 // columns handled at once
-  const int col = threadIdx.x % cols, slice = threadIdx.x / cols;
+  const int g = blockIdx.y, tid = threadIdx.x;
+  const int cols = BL_JOIN / slices, col = tid & (cols - 1), slice = tid / cols;
+  const int e = blockIdx.x * cols + col;
+  double s = 0.0;
+  int c = 0;
+  if (e < a.E) {
+    // (addresses clamped and values masked, so that the loads of a round go out together)
+    const float* part = a.part + (long long)g * a.ctas * a.E + e;
+    const int32_t* cp = (a.idx ? a.cpart : reinterpret_cast<const int32_t*>(a.part)) + (long long)g * a.ctas * a.E + e;
+    const int counted = a.idx ? -1 : 0;
+    constexpr int U = 8;
+    for (int q = slice; q < a.ctas; q += U * slices) {
+      float f[U];
+      int k[U];
+#pragma unroll
+      for (int v = 0; v < U; ++v) {
+        const int at = min(q + v * slices, a.ctas - 1) * a.E;
+        f[v] = __ldcg(part + at);
+        k[v] = __ldcg(cp + at);
+      }
+#pragma unroll
+      for (int v = 0; v < U; ++v) {
+        const bool in = q + v * slices < a.ctas;
+        s += in ? f[v] : 0.f;
+        c += in ? k[v] & counted : 0;
+      }
+    }
+  }
+  su[tid] = s;
+  sc[tid] = c;
+  __syncthreads();
+  if (slice == 0 && e < a.E) {
+    for (int q = 1; q < slices; ++q) {
+      s += su[q * cols + col];
+      c += sc[q * cols + col];
+    }
+    a.usum[(long long)g * a.E + e] = s;
+    a.csum[(long long)g * a.E + e] = c;
+    __threadfence();
+  }
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(&a.done[g], 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+
   double n = 0.0;
-  for (int c = threadIdx.x; c < a.ctas; c += BL_JOIN) n += a.npart[(long long)g * a.ctas + c];
+  for (int q = tid; q < a.ctas; q += BL_JOIN) n += a.npart[(long long)g * a.ctas + q];
   n = block_sum(n, red);
   const double inv_n = n > 0.0 ? 1.0 / n : 0.0;
-  constexpr int PER = BL_MAX_E / BL_JOIN;        // columns per thread at most (sl == 1)
+  constexpr int PER = BL_MAX_E / BL_JOIN;        // columns per thread at most
   double u[PER];
   int cc[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = i * cols + col;
-    double s = 0.0;
-    int c = 0;
-    if (e < a.E && (i == 0 || sl == 1)) {
-      const float* part = a.part + (long long)g * a.ctas * a.E + e;
-      const int32_t* cp = a.cpart + (long long)g * a.ctas * a.E + e;
-      for (int q = slice; q < a.ctas; q += 16 * sl) {
-        float f[16];
-        int k[16];
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const bool in = q + v * sl < a.ctas;
-          f[v] = in ? part[(long long)(q + v * sl) * a.E] : 0.f;
-          k[v] = in && a.idx ? cp[(long long)(q + v * sl) * a.E] : 0;
-        }
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          s += f[v];
-          c += k[v];
-        }
-      }
-    }
-    u[i] = s;
-    cc[i] = c;
-  }
-  if (sl > 1) {
-    su[threadIdx.x] = u[0];
-    sc[threadIdx.x] = cc[0];
-    __syncthreads();
-    if (slice == 0) {
-      for (int q = 1; q < sl; ++q) {
-        u[0] += su[q * cols + col];
-        cc[0] += sc[q * cols + col];
-      }
-    }
-  }
   double csum = 0.0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * cols + col;
-    if (slice == 0 && e < a.E && (i == 0 || sl == 1)) csum += cc[i];
+    const int x = i * BL_JOIN + tid;
+    const long long o = (long long)g * a.E + x;
+    u[i] = x < a.E ? __ldcg(a.usum + o) : 0.0;
+    cc[i] = x < a.E ? __ldcg(a.csum + o) : 0;
+    csum += cc[i];
   }
   csum = block_sum(csum, red);
   const double inv_c = csum > 0.0 ? 1.0 / csum : 0.0;
   double l = 0.0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * cols + col;
-    if (slice == 0 && e < a.E && (i == 0 || sl == 1)) {
+    const int x = i * BL_JOIN + tid;
+    if (x < a.E) {
       const double ue = u[i] * inv_n;
       double ae;
       if (kind == FWPKM_BALANCE_LOAD) {
@@ -275,14 +291,14 @@ balance_join_kernel(BalArgs a, int sl, int kind, float coef, double log_e, float
         ae = ue > 0.0 ? log(ue * a.E) : (ue == 0.0 ? 0.0 : ue);  // NaN stays
         l += ue * (ae - log_e);
       }
-      const long long o = (long long)g * a.E + e;
+      const long long o = (long long)g * a.E + x;
       usage[o] = (float)ue;
       if (counts) counts[o] = cc[i];
       slope[o] = (float)(coef * ae * inv_n);
     }
   }
   l = block_sum(l, red);
-  if (threadIdx.x == 0) loss[g] = (float)(coef * l);
+  if (tid == 0) loss[g] = (float)(coef * l);
 }
 
 template <typename T, int VEC, int NCH, int L>
@@ -366,15 +382,18 @@ size_t bal_carve(const fwpkm_balance_config& c, char* base, BalArgs* a) {
   long long rows;
   split_rows(c, &ctas, &rows);
   const size_t cells = (size_t)c.groups * ctas;
-  const size_t p = b256(4 * cells * c.experts);
+  const size_t p = b256(4 * cells * c.experts), cols = (size_t)c.groups * c.experts;
   if (a) {
     a->part = (float*)base;
     a->cpart = (int32_t*)(base + p);
     a->npart = (int32_t*)(base + 2 * p);
+    a->usum = (double*)(base + 2 * p + b256(4 * cells));
+    a->csum = (int32_t*)(base + 2 * p + b256(4 * cells) + b256(8 * cols));
+    a->done = (int*)(base + 2 * p + b256(4 * cells) + b256(8 * cols) + b256(4 * cols));
     a->ctas = ctas;
     a->rows_cta = rows;
   }
-  return 2 * p + b256(4 * cells);
+  return 2 * p + b256(4 * cells) + b256(8 * cols) + b256(4 * cols) + b256(4 * (size_t)c.groups);
 }
 
 fwpkm_status check_balance(const fwpkm_balance_config* c) {
@@ -492,11 +511,11 @@ fwpkm_status fwpkm_balance_loss(const fwpkm_balance_config* cfg, const void* x, 
   bal_carve(*cfg, (char*)workspace, &r.a);
   const bool ok = cfg->dtype == FWPKM_BF16 ? bal_type<__nv_bfloat16>(r) : bal_type<float>(r);
   if (!ok) return FWPKM_ERR_CUDA;
-  int sl = 1;
-  while (sl < 32 && (long long)sl * 2 * cfg->experts <= BL_JOIN && sl < r.a.ctas) sl <<= 1;
-  launch_k(balance_join_kernel, cfg->groups, BL_JOIN, 0, r.s, r.a, sl, cfg->kind, cfg->coef, log((double)cfg->experts),
-           loss, counts, usage,
-           slope);
+  int slices = 1;  // about eight CTAs' sums per thread, whole warps per slice
+  while (slices < BL_JOIN / 32 && slices * 8 < r.a.ctas) slices <<= 1;
+  const int cols = BL_JOIN / slices;
+  launch_k(balance_join_kernel, dim3((cfg->experts + cols - 1) / cols, cfg->groups), BL_JOIN, 0, r.s, r.a, slices,
+           cfg->kind, cfg->coef, log((double)cfg->experts), loss, counts, usage, slope);
   return bal_done(2);
 }
 
