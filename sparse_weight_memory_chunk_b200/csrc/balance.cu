@@ -121,7 +121,7 @@ __device__ __forceinline__ float team_exp(float (&v)[NV], float* red) {
 }
 
 template <typename T, int VEC, int NCH, int L>
-__global__ void __launch_bounds__(BL_THREADS)
+__global__ void __launch_bounds__(BL_THREADS, L > 32 ? 4 : 1)
 balance_sum_kernel(BalArgs a) {
   constexpr int NV = VEC * NCH;
   constexpr int TEAMS = BL_THREADS / L;
@@ -302,7 +302,7 @@ balance_join_kernel(BalArgs a, int slices, int kind, float coef, double log_e, f
 }
 
 template <typename T, int VEC, int NCH, int L>
-__global__ void __launch_bounds__(BL_THREADS)
+__global__ void __launch_bounds__(BL_THREADS, L > 32 ? 4 : 1)
 balance_grad_kernel(BalArgs a, const float* __restrict__ slope, const float* __restrict__ d_loss, T* __restrict__ dx) {
   constexpr int NV = VEC * NCH;
   constexpr int TEAMS = BL_THREADS / L;
@@ -360,8 +360,10 @@ bool bal_al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t bal_es(int dt) { return dt == FWPKM_BF16 ? 2 : 4; }
 
 // CTAs that the GPU holds at once: a row of up to 1024 logits sits in the registers of a warp
-// twice (its values and the next row's loads).
-int bal_resident(int E) { return 148 * (E > 512 ? 2 : E > 256 ? 3 : 4); }
+// twice (its values and the next row's loads); wider ones are spread over the CTA, whose
+// threads hold 16 of their values (16384 rows of 4096 bf16: 200 us for both directions with two
+// CTAs per SM, 152 with the four that 64 registers a thread allow).
+int bal_resident(int E) { return 148 * (E > 1024 ? 4 : E > 512 ? 2 : E > 256 ? 3 : 4); }
 
 // Rows per CTA of the forward: no more CTAs over all groups than are resident (a second wave of
 // a few doubles the time: 123 us instead of 70 for 16 groups of 4096 x 1024 fp32), and at
