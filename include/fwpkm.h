@@ -495,9 +495,12 @@ fwpkm_status fwpkm_balance_loss_backward(const fwpkm_balance_config* cfg, const 
  *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   S before the first token = s0.
  * log_decay is a constant of the heads (fp32 [H], normally <= 0; -inf: S_t = k_t v_t^T); it
  * gets no gradient.  States are fp32 [B][H][d][d_v], contiguous; q, k, v, o and their
- * gradients fp32 or bf16 (cfg.dtype).  Sums and states are held in fp32; bf16 prompts run
- * on the tensor cores, where fp32 operands enter as enough bf16 pieces that results agree
- * with fp32 arithmetic.
+ * gradients fp32 or bf16 (cfg.dtype).  Sums and states are held in fp32.  bf16 prompts run on
+ * the tensor cores in chunks of 128 tokens: the weighted scores q.k inside a chunk and the
+ * state before it enter o's products rounded once to bf16 (half a step, 2^-9 of a term on
+ * average, beside o's own rounding), the keys in the state as two bf16 pieces, and as three
+ * where the state leaves (sT, ds0: fp32 arithmetic).  A value that is not finite makes what
+ * depends on it not finite, and there also the earlier rows of its chunk.
  * ------------------------------------------------------------------------- */
 
 /* One tensor of all heads: element (b, h, t, e) at p[b*sb + h*sh + t*st + e], any strides of
@@ -525,8 +528,8 @@ fwpkm_status fwpkm_linear_attention_workspace_size(const fwpkm_linattn_config* c
  *          behind them are not read and their rows of o left as they were.
  *   s0     start states or NULL (zeros);  sT  states after each sequence's last token, or
  *          NULL; sT may be s0's memory.
- * T = 0: o is not touched, sT = s0.  The workspace must not be shared with a call that may
- * run at the same time. */
+ * T = 0: o is not touched, sT = s0.  o must not be the memory of q, k or v.  The workspace must
+ * not be shared with a call that may run at the same time. */
 fwpkm_status fwpkm_linear_attention(const fwpkm_linattn_config* cfg, const fwpkm_heads* q, const fwpkm_heads* k,
                                     const fwpkm_heads* v, int T, const float* log_decay, const int32_t* lens,
                                     const float* s0, const fwpkm_heads* o, float* sT, void* workspace,
@@ -534,7 +537,7 @@ fwpkm_status fwpkm_linear_attention(const fwpkm_linattn_config* cfg, const fwpkm
 
 /* Its gradients from d_o (the layout of o) and d_sT (NULL: zero): dq, dk, dv, and ds0 (NULL:
  * not wanted; may be d_sT's memory).  Rows behind a sequence's end are left as they were.
- * dq, dk, dv must not be the memory of q, k, v, d_o. */
+ * dq, dk, dv must not be the memory of q, k, v, d_o or of one another. */
 fwpkm_status fwpkm_linear_attention_backward(const fwpkm_linattn_config* cfg, const fwpkm_heads* q,
                                              const fwpkm_heads* k, const fwpkm_heads* v, int T,
                                              const float* log_decay, const int32_t* lens, const float* s0,
@@ -544,7 +547,8 @@ fwpkm_status fwpkm_linear_attention_backward(const fwpkm_linattn_config* cfg, co
 
 /* Token-at-a-time form: n_tok tokens of every sequence in one launch without a workspace.
  * `state` is read and `state_out` written (the same memory: in place).  lens as above: a
- * sequence with no token keeps its state and its rows of o. */
+ * sequence with no token keeps its state and its rows of o; o must not be the memory of q, k
+ * or v. */
 fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const fwpkm_heads* q, const fwpkm_heads* k,
                                          const fwpkm_heads* v, int n_tok, const float* log_decay,
                                          const int32_t* lens, const float* state, const fwpkm_heads* o,

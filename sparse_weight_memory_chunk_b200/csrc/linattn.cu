@@ -24,6 +24,7 @@
 // 350 us, 49 TFLOP/s.  (With rows staged by plain loads between two barriers the loads'
 // latency bounded it: 128 such heads in 665 us, now 232.)
 #include <cstdio>
+#include <initializer_list>
 
 #include "linattn.cuh"
 #include "sm100.cuh"
@@ -568,6 +569,13 @@ bool heads_ok(const fwpkm_heads* x, const fwpkm_linattn_config& c, bool out, int
   return true;
 }
 
+// Whether an output begins where an input does: another CTA may still have to read what it writes.
+bool shares(const fwpkm_heads* out, std::initializer_list<const fwpkm_heads*> in) {
+  for (const fwpkm_heads* x : in)
+    if (x->p == out->p) return true;
+  return false;
+}
+
 ScanArgs base_args(const fwpkm_linattn_config& c, int T, const float* log_decay, const int32_t* lens) {
   ScanArgs a = {};
   a.log_decay = log_decay; a.lens = lens;
@@ -682,6 +690,7 @@ fwpkm_status fwpkm_linear_attention(const fwpkm_linattn_config* cfg, const fwpkm
   fwpkm_linear_attention_workspace_size(cfg, T, 0, &need);
   if (need > 0 && (!workspace || !la_al(workspace, 256))) return FWPKM_ERR_INVALID_ARG;
   if (ws_bytes < need) return FWPKM_ERR_WORKSPACE;
+  if (T > 0 && shares(o, {q, k, v})) return FWPKM_ERR_INVALID_ARG;
   cudaGetLastError();
   PdlScope pdl(true);
   return la_done(run_pass(a, cfg->dtype, (float*)workspace, (cudaStream_t)stream));
@@ -719,6 +728,8 @@ fwpkm_status fwpkm_linear_attention_backward(const fwpkm_linattn_config* cfg, co
   fwpkm_linear_attention_workspace_size(cfg, T, 1, &need);
   if (need > 0 && (!workspace || !la_al(workspace, 256))) return FWPKM_ERR_INVALID_ARG;
   if (ws_bytes < need) return FWPKM_ERR_WORKSPACE;
+  if (T > 0 && (shares(dq, {q, k, v, d_o, dk, dv}) || shares(dk, {q, k, v, d_o, dv}) || shares(dv, {q, k, v, d_o})))
+    return FWPKM_ERR_INVALID_ARG;
   cudaGetLastError();
   PdlScope pdl(true);
   int nl = 0;
@@ -749,6 +760,7 @@ fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const 
       return FWPKM_ERR_INVALID_ARG;
     a.q = *q; a.k = *k; a.v = *v; a.o = *o;
   }
+  if (n_tok > 0 && shares(o, {q, k, v})) return FWPKM_ERR_INVALID_ARG;
   a.s_in = state;
   a.s_out = state_out;
   cudaGetLastError();

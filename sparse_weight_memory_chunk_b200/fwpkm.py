@@ -281,7 +281,8 @@ def addressing_metrics(idx, N: int, window: int = 32768, workspace=None, stream=
 
 # ---- operators around the memory -------------------------------------------------------
 # Torch tensors in, torch tensors out; every call only enqueues on `stream` (default: the
-# current stream of the tensors' device).  Single tokens and small batches take about as long
+# current stream of the tensors' device; for another one the caller keeps the inputs alive and
+# waits, as for any kernel there).  Single tokens and small batches take about as long
 # on the host as on the GPU, so the checks below stay with what costs little.
 
 def _need(ok, what):
@@ -332,13 +333,23 @@ def _side(t, like, dtype, shape, what):
     return t.data_ptr()
 
 
-def _scratch(workspace, nbytes, like, what):
+def _empty(stream, shape, dtype, like):
+    """A new tensor on `like`'s device.  With a stream given it comes from that stream's memory:
+    the current one's may still be in use, or be handed out again, while the call runs there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scratch(workspace, nbytes, like, stream, what):
     """(tensor, pointer, bytes) of a workspace: the caller's, or a new one of nbytes."""
     if workspace is None:
         if not nbytes:
             return None, None, 0
         import torch
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace = _empty(stream, nbytes, torch.uint8, like)
         return workspace, workspace.data_ptr(), nbytes
     _need(workspace.device == like.device and workspace.is_contiguous(),
           f"{what}: the workspace must be contiguous, on {like.device}")
@@ -377,7 +388,7 @@ def lookup(table, idx, w=None, scale=1.0, out=None, stream=None):
     Indices outside the table read zeros."""
     cfg, shape, n = _lookup_config(table, idx, w, scale)
     if out is None:
-        out = table.new_empty(shape)
+        out = _empty(stream, shape, table.dtype, table)
     else:
         _side(out, table, table.dtype, shape, "out")
     _call(table, stream, "lookup", lib().fwpkm_lookup, ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
@@ -402,7 +413,7 @@ def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumula
     _need(d_out is not None, "d_out is needed")
     _need(not accumulate or d_table is not None, "accumulate needs the d_table to add to")
     if d_table is None:
-        d_table = torch.empty(table.shape, dtype=grad_dtype or table.dtype, device=table.device)
+        d_table = _empty(stream, table.shape, grad_dtype or table.dtype, table)
     _need(d_table.shape == table.shape and d_table.device == table.device
           and (d_table.stride(1) == 1 or table.shape[1] <= 1)
           and (table.shape[0] <= 1 or d_table.stride(0) >= table.shape[1]),
@@ -411,13 +422,13 @@ def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumula
     if w is None or not need_dw:
         _need(dw is None, "dw needs w and need_dw")
     elif dw is None:
-        dw = torch.empty(idx.shape, dtype=torch.float32, device=table.device)
+        dw = _empty(stream, idx.shape, torch.float32, table)
     else:
         _side(dw, table, torch.float32, idx.shape, "dw")
     L, c = lib(), ctypes.byref(cfg)
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
                             _bytes(L.fwpkm_lookup_backward_workspace_size, "lookup_backward", c, n), table,
-                            "lookup_backward")
+                            stream, "lookup_backward")
     _call(table, stream, "lookup_backward", L.fwpkm_lookup_backward, c, table.data_ptr(), idx.data_ptr(),
           None if w is None else w.data_ptr(), p_out, n, d_table.data_ptr(), max(d_table.stride(0), table.shape[1]),
           _dtype(d_table, "d_table"), int(accumulate), None if dw is None else dw.data_ptr(), pw, nw)
@@ -457,12 +468,12 @@ def balance_loss(x, idx=None, mask=None, kind="load", coef=1.0, workspace=None, 
     G, E = cfg.groups, cfg.experts
     L, c = lib(), ctypes.byref(cfg)
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
-                            _bytes(L.fwpkm_balance_workspace_size, "balance_loss", c), x, "balance_loss")
+                            _bytes(L.fwpkm_balance_workspace_size, "balance_loss", c), x, stream, "balance_loss")
     r = BalanceLoss()
     r.kind, r.coef = kind, coef
-    f = torch.empty(2 * G * E + G, dtype=torch.float32, device=x.device)
+    f = _empty(stream, 2 * G * E + G, torch.float32, x)
     r.usage, r.slope, r.loss = f[:G * E].view(G, E), f[G * E:2 * G * E].view(G, E), f[2 * G * E:]
-    r.counts = None if idx is None else torch.empty(G, E, dtype=torch.int32, device=x.device)
+    r.counts = None if idx is None else _empty(stream, (G, E), torch.int32, x)
     p = f.data_ptr()
     _call(x, stream, "balance_loss", L.fwpkm_balance_loss, c, x.data_ptr(), None if idx is None else idx.data_ptr(),
           None if mask is None else mask.data_ptr(), pw, nw, p + 8 * G * E, None if idx is None else r.counts.data_ptr(),
@@ -479,7 +490,7 @@ def balance_loss_backward(x, result: BalanceLoss, mask=None, d_loss=None, dx=Non
     ps = _side(result.slope, x, torch.float32, (G, E), "result.slope")
     pl = _side(d_loss, x, torch.float32, (G,), "d_loss")
     if dx is None:
-        dx = torch.empty(G, T, E, dtype=x.dtype, device=x.device)
+        dx = _empty(stream, (G, T, E), x.dtype, x)
     else:
         _side(dx, x, x.dtype, (G, T, E), "dx")
     _call(x, stream, "balance_loss_backward", lib().fwpkm_balance_loss_backward, ctypes.byref(cfg), x.data_ptr(),
@@ -510,9 +521,9 @@ def _linattn_args(q, k, v, log_decay, scale, lens):
     return ctypes.byref(LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale)), hq, hk, hv, ld, ln, B, H, T, d, dv
 
 
-def _rows_like(t, B, H, T, w):
+def _rows_like(t, B, H, T, w, stream):
     """A new [B][H][T][w] tensor in the memory order [B][T][H][w] of a projection's output."""
-    return t.new_empty((B, T, H, w)).transpose(1, 2)
+    return _empty(stream, (B, T, H, w), t.dtype, t).transpose(1, 2)
 
 
 def linear_attention_workspace_size(q, v, backward=False) -> int:
@@ -530,15 +541,15 @@ def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, 
     import torch
     c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
-        o = _rows_like(v, B, H, T, dv)
+        o = _rows_like(v, B, H, T, dv, stream)
     ho = _heads(o, q, (B, H, T, dv), "o")
     if sT is None and final_state:
-        sT = torch.empty(B, H, d, dv, dtype=torch.float32, device=q.device)
+        sT = _empty(stream, (B, H, d, dv), torch.float32, q)
     p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
     pT = _side(sT, q, torch.float32, (B, H, d, dv), "sT")
     L = lib()
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
-                            _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention", c, T, 0), q,
+                            _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention", c, T, 0), q, stream,
                             "linear_attention")
     _call(q, stream, "linear_attention", L.fwpkm_linear_attention, c, hq, hk, hv, T, ld, ln, p0, ho, pT, pw, nw)
     return o, sT
@@ -553,16 +564,16 @@ def linear_attention_backward(q, k, v, log_decay, d_o, scale=1.0, s0=None, d_sT=
     c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
     ho = _heads(d_o, q, (B, H, T, dv), "d_o")
     if grads is None:
-        grads = (_rows_like(q, B, H, T, d), _rows_like(q, B, H, T, d), _rows_like(v, B, H, T, dv))
+        grads = tuple(_rows_like(q, B, H, T, w, stream) for w in (d, d, dv))
     hg = [_heads(t, q, (B, H, T, w), n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
     if ds0 is None and state_grad:
-        ds0 = torch.empty(B, H, d, dv, dtype=torch.float32, device=q.device)
+        ds0 = _empty(stream, (B, H, d, dv), torch.float32, q)
     p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
     pT = _side(d_sT, q, torch.float32, (B, H, d, dv), "d_sT")
     pd = _side(ds0, q, torch.float32, (B, H, d, dv), "ds0")
     L = lib()
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
-                            _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention_backward", c, T, 1), q,
+                            _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention_backward", c, T, 1), q, stream,
                             "linear_attention_backward")
     _call(q, stream, "linear_attention_backward", L.fwpkm_linear_attention_backward, c, hq, hk, hv, T, ld, ln, p0, ho,
           pT, *hg, pd, pw, nw)
@@ -577,12 +588,12 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
     import torch
     c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
-        o = _rows_like(v, B, H, T, dv)
+        o = _rows_like(v, B, H, T, dv, stream)
     ho = _heads(o, q, (B, H, T, dv), "o")
     _need(state is not None, "state is needed")
     ps = _side(state, q, torch.float32, (B, H, d, dv), "state")
     if state_out is None:
-        state_out = state if in_place else torch.empty_like(state)
+        state_out = state if in_place else _empty(stream, state.shape, torch.float32, q)
     po = _side(state_out, q, torch.float32, (B, H, d, dv), "state_out")
     _call(q, stream, "linear_attention_step", lib().fwpkm_linear_attention_step, c, hq, hk, hv, T, ld, ln, ps, ho, po)
     return o, state_out
@@ -592,7 +603,7 @@ def linear_attention_sync(device=None, stream=None):
     """fwpkm_linear_attention_sync: wait for the stream and raise what linear-attention kernels
     on the device have latched (a wait that timed out)."""
     import torch
-    with torch.cuda.device(device):
+    with torch.cuda.device(device if stream is None else stream.device):
         handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
         _check(lib().fwpkm_linear_attention_sync(handle), "linear_attention_sync")
 
