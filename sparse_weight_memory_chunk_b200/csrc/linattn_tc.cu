@@ -65,11 +65,11 @@ constexpr int LA_BLOCK = LC * 128;       // bytes of a 64-column block of 128 ro
 __device__ int g_la_status = DEV_OK;     // latched by a kernel whose wait ran out
 
 // TMEM columns
-constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_K1 = 448, TM_COLS = 512;
+constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_COLS = 512;  // (a piece: 64)
 
 struct TcBars {
-  uint64_t full_q, full_k[2], full_v[2], free_k[2], o2[2];
-  uint64_t p, o1, staged, kt, khi, u1, mid, u2, est, ofree, ufree, cleared, store, drain, stall;
+  uint64_t full_q, full_k[2], full_v[2], free_k[2], o2[2], kt[2], u2[2];
+  uint64_t p, o1, staged, khi, u1, mid, est, ofree, ufree, cleared, store, drain, stall;
 };
 
 template <int DK, int DV>
@@ -180,14 +180,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       mbar_init(&bar->full_v[i], 1);
       mbar_init(&bar->free_k[i], 1);
       mbar_init(&bar->o2[i], 1);
+      mbar_init(&bar->kt[i], LA_GROUP_WARPS);
+      mbar_init(&bar->u2[i], 1);
     }
     mbar_init(&bar->p, 1);
     mbar_init(&bar->o1, 1);
-    mbar_init(&bar->kt, LA_GROUP_WARPS);
     mbar_init(&bar->khi, LA_GROUP_WARPS);
     mbar_init(&bar->u1, 1);
     mbar_init(&bar->mid, LA_GROUP_WARPS);
-    mbar_init(&bar->u2, 1);
     mbar_init(&bar->est, LA_GROUP_WARPS);
     mbar_init(&bar->ofree, LA_GROUP_WARPS);
     mbar_init(&bar->ufree, LA_GROUP_WARPS);
@@ -304,19 +304,23 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         };
         const bool state = init != nullptr || c > 0;
         {  // (ufree: the U of the chunk before has been taken up by the state)
-          const Wait kt{&bar->kt, ph};
+          const Wait kt{&bar->kt[ph], ph2};
           ok = la_wait_each(lane, abort, kt, {&bar->full_v[ph], ph2}, {&bar->full_k[ph], ph2},
                             c == 0 ? kt : Wait{&bar->ufree, ph ^ 1});
         }
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          u_piece(TM_K0, true);
-          u_piece(TM_K1, false);
-          umma_commit(three ? &bar->u1 : &bar->u2);
+          const uint32_t at = local && ph ? TM_P : TM_K0;
+          u_piece(at, true);
+          u_piece(at + 64, false);
+          if (local && three) u_piece(TM_O + ph * 64, false);
+          umma_commit(three && !local ? &bar->u1 : &bar->u2[ph]);
+          if (local) umma_commit(&bar->free_k[ph]);  // K and V
         }
         __syncwarp();
-        if (!local) {
+        if (local) continue;
+        {
           // (o2 of the chunk before: P's columns are free)
           const Wait q{&bar->full_q, ph};
           ok = la_wait_each(lane, abort, q, c == 0 ? q : Wait{&bar->o2[ph ^ 1], (uint32_t)(((c - 1) >> 1) & 1)}, q, q);
@@ -340,14 +344,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           tc_fence_after();
           if (elect_one()) {
             u_piece(TM_K0, false);
-            umma_commit(&bar->u2);
+            umma_commit(&bar->u2[ph]);
           }
           __syncwarp();
-        }
-        if (local) {
-          if (elect_one()) umma_commit(&bar->free_k[ph]);  // K and V
-          __syncwarp();
-          continue;
         }
         // E's pieces, and O's columns (the rows of the previous chunk have left)
         const Wait est{&bar->est, ph};
@@ -424,10 +423,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (lane == 0) mbar_arrive(&bar->cleared);
         if (!la_wait_warp(&bar->cleared, 1, abort)) break;
       }
-      // the previous chunk's U has read the pieces
-      if (c > 0 && !la_wait_warp(&bar->u2, ph ^ 1, abort)) break;
+      // the U that read the pieces' columns before has finished: the chunk before's, or of a pass
+      // that forms states only, which has two sets of columns, the one's before that
+      if (local ? c > 1 && !la_wait_warp(&bar->u2[ph], ph2 ^ 1, abort)
+                : c > 0 && !la_wait_warp(&bar->u2[ph ^ 1], ((c - 1) >> 1) & 1, abort))
+        break;
       tc_fence_after();
-      const uint32_t kt = smem_u32(kb) + k_at;
+      const uint32_t kt = smem_u32(kb) + k_at, pieces = local && ph ? TM_P : TM_K0;
       uint32_t khi[8][4];                           // [16 tokens, lane half][.]
 #pragma unroll
       for (int q = 0; q < 4; ++q) {                 // 16 tokens
@@ -455,16 +457,21 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + q * 8;
-          tmem_st_16x128_x2(at + TM_K0, lo[u]);
-          tmem_st_16x128_x2(at + TM_K1, md[u]);
+          const uint32_t at = lanes + ((uint32_t)(u * 16) << 16) + q * 8 + pieces;
+          tmem_st_16x128_x2(at, lo[u]);
+          tmem_st_16x128_x2(at + 64, md[u]);
         }
+      }
+      if (three && local) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          tmem_st_16x128_x2(lanes + ((uint32_t)((i & 1) * 16) << 16) + (i >> 1) * 8 + TM_O + ph * 64, khi[i]);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->kt);
-      if (three) {
+      if (lane == 0) mbar_arrive(&bar->kt[ph]);
+      if (three && !local) {
         // the keys' high piece takes the low one's place once that has been read
         if (!la_wait_warp(&bar->u1, ph, abort)) break;
         tc_fence_after();
@@ -626,7 +633,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const uint32_t ph = c & 1;
       const int m = tokens(c);
       // E' = a^len E + U
-      if (!la_wait_warp(&bar->u2, ph, abort)) break;
+      if (!la_wait_warp(&bar->u2[ph], (c >> 1) & 1, abort)) break;
       tc_fence_after();
       {
         const int len = m - (c == 0 && ready0 ? 1 : 0);
