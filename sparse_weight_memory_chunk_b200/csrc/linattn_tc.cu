@@ -169,7 +169,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   const ScanArgs& a = ps.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool local = ps.local != 0;
-  const bool three = a.s_out != nullptr;  // the state leaves in fp32
+  // whether this segment's state leaves in fp32 (by itself, or through the states after it)
+  const bool three = a.s_out != nullptr && (local || (int)blockIdx.y == a.nseg - 1);
   const int bh = blockIdx.x, g = blockIdx.y;
   const int b = bh / a.H, h = bh - b * a.H;
 
@@ -573,34 +574,43 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     // States in global memory go through the room of E's pieces when their rows are contiguous
     // (fp32 d x DV, 16-byte chunks swizzled by row: a thread's own row directly would touch 32
     // rows per access); transposed ones are contiguous across the lanes.
-    float S[EC];
-#pragma unroll
-    for (int j = 0; j < EC; ++j) S[j] = 0.f;
     constexpr int CH = DV / 4;
     auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(so + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
+    float S[EC];
     if (init) {
       if (isj == 1 && (a.dv & 3) == 0 && ((uintptr_t)init & 15) == 0 && (isi & 3) == 0) {
-        for (int x = mt; x < a.d * CH; x += LA_GROUP) {
-          const int r = x / CH, ch = x - r * CH;
-          *chunk_at(r, ch) = 4 * ch < a.dv ? *reinterpret_cast<const float4*>(init + r * isi + 4 * ch)
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        st_sync();
-        if (row < a.d) {
+        // (eight loads in flight: one after the other they took 10 us)
+#pragma unroll 1
+        for (int x0 = mt; x0 < a.d * CH; x0 += 8 * LA_GROUP) {
+          float4 y[8];
 #pragma unroll
-          for (int j = 0; j < EC; j += 4) {
-            const float4 x = *chunk_at(row, (j0 + j) >> 2);
-            S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+          for (int i = 0; i < 8; ++i) {
+            const int x = x0 + i * LA_GROUP, r = x / CH, ch = x - r * CH;
+            y[i] = r < a.d && 4 * ch < a.dv ? *reinterpret_cast<const float4*>(init + r * isi + 4 * ch)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int x = x0 + i * LA_GROUP, r = x / CH;
+            if (r < a.d) *chunk_at(r, x - r * CH) = y[i];
           }
         }
         st_sync();
-      } else if (row < a.d) {
 #pragma unroll
-        for (int j = 0; j < EC; ++j)
-          if (j0 + j < a.dv) S[j] = init[row * isi + (j0 + j) * isj];
+        for (int j = 0; j < EC; j += 4) {
+          const float4 x = row < a.d ? *chunk_at(row, (j0 + j) >> 2) : make_float4(0.f, 0.f, 0.f, 0.f);
+          S[j] = x.x; S[j + 1] = x.y; S[j + 2] = x.z; S[j + 3] = x.w;
+        }
+        st_sync();
+      } else {
+#pragma unroll
+        for (int j = 0; j < EC; ++j) S[j] = row < a.d && j0 + j < a.dv ? init[row * isi + (j0 + j) * isj] : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < EC; ++j) S[j] *= in_scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < EC; ++j) S[j] = 0.f;
     }
     auto put_state = [&](float f) {  // f E in bf16, the second operand of Q E
       if (row < DK) {
