@@ -495,7 +495,7 @@ sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, i
 // reads to SEG terms plus its partials.
 // ---------------------------------------------------------------------------
 constexpr int SEG = 32;
-constexpr int ZERO_ROWS = 8, ZERO_BYTES = 8192;
+constexpr int ZERO_BYTES = 8192;
 
 struct SegArgs {
   const uint2* item;  // sorted (row, pair)
@@ -561,16 +561,32 @@ __device__ __forceinline__ void get_part(const float* d, float (&x)[VEC]) {
   }
 }
 
-// Whether `row` occurs in the sorted keys.
-__device__ __forceinline__ bool has_row(const uint2* __restrict__ item, long long P, uint32_t row) {
-  long long lo = 0, hi = P;
+// Whether `row` occurs in the sorted keys [lo, end).
+__device__ __forceinline__ bool has_row(const uint2* __restrict__ item, long long lo, long long end, uint32_t row) {
+  long long hi = end;
   while (lo < hi) {
     const long long mid = (lo + hi) >> 1;
     if (__ldg(&item[mid].x) < row) lo = mid + 1;
     else hi = mid;
   }
-  return lo < P && __ldg(&item[lo].x) == row;
+  return lo < end && __ldg(&item[lo].x) == row;
 }
+// The first of the sorted keys [lo, hi) that is not below `row` (hi: none), by a whole warp: 32
+// probes a step.
+__device__ __forceinline__ long long first_key(const uint2* __restrict__ item, long long lo, long long hi,
+                                               long long row, int lane) {
+  while (hi - lo > 32) {
+    const long long step = (hi - lo + 31) / 32, at = lo + lane * step + step - 1;
+    lo += __popc(__ballot_sync(0xffffffffu, at < hi && (long long)__ldg(&item[at].x) < row)) * step;
+    if (lo + step - 1 < hi) hi = lo + step - 1;
+  }
+  return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && (long long)__ldg(&item[lo + lane].x) < row));
+}
+// Rows that a warp of the zeroing CTAs takes at once: about 64 KB of wide ones (their stores are
+// the work), else one per lane (finding them is: 408100 rows of 64 fp32 that 12149 pairs leave
+// took 98 us with eight rows, each searched for among all pairs, 61 with 32 among the pairs of the
+// warp's rows).
+__host__ __device__ constexpr int zero_rows(long long row_bytes) { return row_bytes >= 2048 ? 8 : 32; }
 
 // ACC: added to d_table, whose rows are loaded with the pairs (SEG_U pairs in flight per team).
 template <typename T, typename G, int VEC, bool ACC>
@@ -579,9 +595,9 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   pdl_wait();
   pdl_trigger();
   if ((int)blockIdx.x >= sum_blocks) {
-    // ---- rows no pair reads: zero (dense gradient only).  A warp takes ZERO_ROWS rows, a lane
-    // looks each of them up in the sorted keys, then the missing ones are written: by bulk
-    // copies of zeros from shared memory where rows are on the 16-byte grid
+    // ---- rows no pair reads: zero (dense gradient only).  A warp takes a few rows, finds the
+    // sorted keys among them, a lane looks each row up there, and the missing ones are written: by
+    // bulk copies of zeros from shared memory where rows are on the 16-byte grid
     __shared__ __align__(16) uint8_t zeros[VEC == 1 ? 16 : ZERO_BYTES];
     if (VEC > 1) {
       for (int i = threadIdx.x * 16; i < ZERO_BYTES; i += LK_THREADS * 16)
@@ -592,9 +608,11 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)(gridDim.x - sum_blocks) * (LK_THREADS / 32);
     const long long w0 = (long long)(blockIdx.x - sum_blocks) * (LK_THREADS / 32) + (threadIdx.x >> 5);
-    for (long long r0 = w0 * ZERO_ROWS; r0 < a.rows; r0 += warps * ZERO_ROWS) {
+    const int each = zero_rows((long long)a.width * sizeof(G));
+    for (long long r0 = w0 * each; r0 < a.rows; r0 += warps * each) {
       const long long r = r0 + lane;
-      const bool zero = lane < ZERO_ROWS && r < a.rows && !has_row(a.item, a.P, (uint32_t)r);
+      const long long lo = first_key(a.item, 0, a.P, r0, lane), hi = first_key(a.item, lo, a.P, r0 + each, lane);
+      const bool zero = lane < each && r < a.rows && !has_row(a.item, lo, hi, (uint32_t)r);
       if (VEC > 1) {
         if (zero) {
           const long long bytes = (long long)a.width * sizeof(G);
@@ -940,11 +958,12 @@ int go_sum(const fwpkm_lookup_config& c, SegArgs a, const void* d_out, void* d_t
   const int ty = LK_THREADS / a.tx_n;
   const unsigned gy = (unsigned)((a.vecs + a.tx_n - 1) / a.tx_n);
   const unsigned sb = (unsigned)((a.ranges + ty - 1) / ty);
-  // dense gradient: CTAs that zero the rows nothing reads, 64 rows each (up to 16 per SM's
+  // dense gradient: CTAs that zero the rows nothing reads, a few rows per warp (up to 16 per SM's
   // place, then more; column blocks share one row split: only blockIdx.y == 0 has them)
   long long zb = 0;
   if (!ACC) {
-    zb = (a.rows + 63) / 64;
+    const int each = LK_THREADS / 32 * zero_rows((long long)c.width * sizeof(G));
+    zb = (a.rows + each - 1) / each;
     if (zb > 148 * 32) zb = 148 * 32;
   }
   if (sb + zb == 0) return 0;

@@ -138,12 +138,6 @@ __device__ __forceinline__ void mul2(float& x, float& y, float u, float v) {
       : "+f"(x), "+f"(y)
       : "f"(u), "f"(v));
 }
-__device__ __forceinline__ void sub2(float& x, float& y, float u, float v) {
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n sub.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, "
-      "a;\n}\n"
-      : "+f"(x), "+f"(y)
-      : "f"(u), "f"(v));
-}
 // x += a c, y += b d
 __device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c, float d) {
   asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mov.b64 r, {%4, %5};\n"
