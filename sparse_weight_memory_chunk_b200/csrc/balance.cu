@@ -438,7 +438,7 @@ template <typename T, int VEC, int NCH, int L>
 bool bal_go(const BalRun& r) {
   if (!r.grad) {
     const size_t smem = 4 * ((size_t)BL_THREADS * VEC * NCH) + (r.a.idx ? 4 * (size_t)r.a.E : 0);
-    if (smem > 48 * 1024 && !raise_smem_limit((const void*)balance_sum_kernel<T, VEC, NCH, L>, smem)) return false;
+    if (smem > 47 * 1024 && !raise_smem_limit((const void*)balance_sum_kernel<T, VEC, NCH, L>, smem)) return false;
     launch_k(balance_sum_kernel<T, VEC, NCH, L>, dim3(r.a.ctas, r.a.G), BL_THREADS, smem, r.s, r.a);
   } else {
     constexpr int TEAMS = BL_THREADS / L;

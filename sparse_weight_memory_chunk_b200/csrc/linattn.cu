@@ -493,10 +493,11 @@ int go_scan(const ScanArgs& a, int local, cudaStream_t s) {
   const int rg = SC_THREADS / sh.lj, dp = rg * sh.ni, cols = 4 * sh.lj;
   const size_t smem = SC_TB * ((size_t)4 * SC_WARPS * cols + 2 * sizeof(T) * (2 * dp + cols));
   const int unit = copy_unit<T>(a, cols);
+  // (the 48 KB that need no leave hold the kernel's static tables too)
   const dim3 grid((unsigned)((long long)a.B * a.H * sh.tiles), local ? a.nseg - 1 : a.nseg);
 #define FWPKM_SCAN(NI)                                                                           \
   case NI:                                                                                       \
-    if (smem > 48 * 1024 && !raise_smem_limit((const void*)scan_kernel<T, NI>, smem)) return -1; \
+    if (smem > 47 * 1024 && !raise_smem_limit((const void*)scan_kernel<T, NI>, smem)) return -1; \
     launch_k(scan_kernel<T, NI>, grid, SC_THREADS, smem, s, a, sh.lj, unit, local);               \
     break;
   switch (sh.ni) {
