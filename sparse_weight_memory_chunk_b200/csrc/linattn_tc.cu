@@ -631,7 +631,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       if (lane == 0) mbar_arrive(&bar->est);
     };
     const bool ready0 = g == 0 && a.in_ready;       // the first chunk's E is decayed already
-    if (!local) {
+    // (without a chunk nothing reads E, whose room the last state passes through)
+    if (!local && chunks > 0) {
       if (init) put_state(fast ? decay_pow(ld, (float)(LC - (ready0 ? 1 : 0))) : 1.f);
       else if (lane == 0) mbar_arrive(&bar->est);
     }
