@@ -23,8 +23,8 @@
 // kept in fp32 registers and U is a fresh accumulator per chunk, so the tensor cores' running
 // sums span one chunk only.
 //
-// CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one;
-// the rows of O leave through shared memory), warp 1 owns TMEM and issues the MMAs (one thread),
+// CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one, the
+// rows of O through shared memory; a pass that only forms segment states: K, V three stages), warp 1 owns TMEM and issues the MMAs (one thread),
 // warps 4-11 weight the keys, 12-19 the scores, 20-27 carry the state and the output: a warp
 // reads TMEM lanes 32 (w % 4).. and one half of the columns.  TMEM (512 columns): P fp32,
 // overwritten in place by its bf16 pairs (operand A of P V); O; U; two pieces of the
@@ -34,10 +34,15 @@
 //   keys          K hi(c)              K pieces(c+1)
 //   scores                        P bf16(c)
 //   state   O out(c-1)                 E(c)      E bf16(c+1)
-// so the MMAs of a chunk (6 products of 128^3, 3072 cycles at the dense rate) follow one another
-// while the groups work beside them.  (With the groups' steps done in turn by the same warps a
-// chunk took the sum of their latencies, 5.5 us of 148 heads at d = d_v = 128.)
-// Bound: HBM for d = d_v = 128 (128 KB per chunk, 5500 cycles of an SM's share at 6.46 TB/s).
+// so the MMAs of a chunk (6 products of 128^3, 3072 cycles at the dense rate; 5 where no state
+// leaves) follow one another while the groups work beside them.  (With the groups' steps done in
+// turn by the same warps a chunk took the sum of their latencies, 5.5 us of 148 heads at
+// d = d_v = 128.)  A pass that only forms segment states has TMEM to spare and keeps two sets of
+// key pieces, so that weighting a chunk's keys overlaps the products of the one before.
+// Bound: for d = d_v = 128 a chunk is 128 KB, 3.0 us of an SM's share of the copy bandwidth; 148
+// heads of 8192 tokens take 4.2 us a chunk (72% of it), 4.5 with the final state (tensor pipe 38%
+// active, issue slots 50%): what is left is the chain state -> E bf16 -> Q E -> next state, and
+// keys -> U -> next keys.
 #include <cstdio>
 
 #include "linattn.cuh"
@@ -68,7 +73,7 @@ __device__ int g_la_status = DEV_OK;     // latched by a kernel whose wait ran o
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_COLS = 512;  // (a piece: 64)
 
 struct TcBars {
-  uint64_t full_q, full_k[2], full_v[2], free_k[2], o2[2], kt[2], u2[2];
+  uint64_t full_q, full_k[3], full_v[3], free_k[3], o2[2], kt[2], u2[2];
   uint64_t p, o1, staged, khi, u1, mid, est, ofree, ufree, cleared, store, drain, stall;
 };
 
@@ -176,10 +181,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->full_q, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&bar->full_k[i], 1);
       mbar_init(&bar->full_v[i], 1);
       mbar_init(&bar->free_k[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->o2[i], 1);
       mbar_init(&bar->kt[i], LA_GROUP_WARPS);
       mbar_init(&bar->u2[i], 1);
@@ -235,6 +242,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   auto tile_t = [&](int c) { return a.reverse ? n - (t0 + c * LC) - LC : t0 + c * LC; };
   auto tokens = [&](int c) { return min(LC, t1 - t0 - c * LC); };
 
+  // K and V: two stages, and where only states are formed a third in the room of Q and of O
+  const int stages = local ? 3 : 2;
+  auto stage = [&](int c) { return local ? c % 3 : c & 1; };
+  auto stage_ph = [&](int c) { return (uint32_t)((local ? c / 3 : c >> 1) & 1); };
+  auto k_rows = [&](int st) { return st == 2 ? sq : sk + st * SM::K; };
+  auto v_rows = [&](int st) { return st == 2 ? so : sv + st * SM::V; };
+
   int k_loads = 0, v_loads = 0, q_loads = 0;  // producer: chunks whose loads were issued
   if (warp < LA_ROLE_WARPS) regs_dec<LA_ROLE_REGS>();
   if (warp == 0) {
@@ -247,12 +261,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       };
       auto load_k = [&](int c) {
         if (c >= chunks) return;
-        load(&mk, sk + (c & 1) * SM::K, DK, &bar->full_k[c & 1], ps.ck, c);
+        load(&mk, k_rows(stage(c)), DK, &bar->full_k[stage(c)], ps.ck, c);
         ++k_loads;
       };
       auto load_v = [&](int c) {
         if (c >= chunks) return;
-        load(&mv, sv + (c & 1) * SM::V, DV, &bar->full_v[c & 1], ps.cv, c);
+        load(&mv, v_rows(stage(c)), DV, &bar->full_v[stage(c)], ps.cv, c);
         ++v_loads;
       };
       auto load_q = [&](int c) {
@@ -263,14 +277,16 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       load_k(0);
       load_v(0);
       load_q(0);
-      load_k(1);
-      load_v(1);
+      for (int c = 1; c < stages; ++c) {
+        load_k(c);
+        load_v(c);
+      }
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = (c >> 1) & 1;
-        if (!la_wait(&bar->free_k[c & 1], ph, abort)) break;
-        load_k(c + 2);
+        if (!la_wait(&bar->free_k[stage(c)], stage_ph(c), abort)) break;
+        load_k(c + stages);
         if (local) {
-          load_v(c + 2);
+          load_v(c + stages);
           continue;
         }
         if (!la_wait(&bar->o1, c & 1, abort)) break;
@@ -296,7 +312,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       bool ok = !(ps.stall && !la_wait_warp(&bar->stall, 0, abort));
       for (int c = 0; c < chunks && ok; ++c) {
         const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
-        const uint32_t k0 = smem_u32(sk + ph * SM::K), v0 = smem_u32(sv + ph * SM::V);
+        const int st = stage(c);
+        const uint32_t k0 = smem_u32(k_rows(st)), v0 = smem_u32(v_rows(st)), st_ph = stage_ph(c);
         const uint64_t vd = sdesc_mn_sw128(v0, LA_BLOCK);   // + 128 per 16 tokens (16-byte units)
         auto u_piece = [&](uint32_t at, bool first) {
 #pragma unroll 2
@@ -306,7 +323,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const bool state = init != nullptr || c > 0;
         {  // (ufree: the U of the chunk before has been taken up by the state)
           const Wait kt{&bar->kt[ph], ph2};
-          ok = la_wait_each(lane, abort, kt, {&bar->full_v[ph], ph2}, {&bar->full_k[ph], ph2},
+          ok = la_wait_each(lane, abort, kt, {&bar->full_v[st], st_ph}, {&bar->full_k[st], st_ph},
                             c == 0 ? kt : Wait{&bar->ufree, ph ^ 1});
         }
         if (!ok) break;
@@ -317,7 +334,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           u_piece(at + 64, false);
           if (local && three) u_piece(TM_O + ph * 64, false);
           umma_commit(three && !local ? &bar->u1 : &bar->u2[ph]);
-          if (local) umma_commit(&bar->free_k[ph]);  // K and V
+          if (local) umma_commit(&bar->free_k[st]);  // K and V
         }
         __syncwarp();
         if (local) continue;
@@ -336,7 +353,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 umma_bf16(tmem + TM_P, qd + x * (LA_BLOCK >> 4) + kk * 2, kd + x * (LA_BLOCK >> 4) + kk * 2, id_p,
                           (x | kk) != 0 ? 1u : 0u);
             umma_commit(&bar->p);
-            umma_commit(&bar->free_k[ph]);
+            umma_commit(&bar->free_k[st]);
           }
           __syncwarp();
         }
@@ -349,7 +366,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           }
           __syncwarp();
         }
-        // E's pieces, and O's columns (the rows of the previous chunk have left)
+        // E in bf16, and O's columns (the rows of the previous chunk have left)
         const Wait est{&bar->est, ph};
         ok = la_wait_each(lane, abort, est, c == 0 ? est : Wait{&bar->ofree, ph ^ 1}, est, est);
         if (!ok) break;
@@ -362,7 +379,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
               umma_bf16(tmem + TM_O, qd + (kk >> 2) * (LA_BLOCK >> 4) + (kk & 3) * 2, ed + kk * 128, id_v,
                         kk != 0 ? 1u : 0u);
           }
-          umma_commit(&bar->o1);  // also: Q and E's pieces have been read
+          umma_commit(&bar->o1);  // also: Q and E have been read
         }
         __syncwarp();
         if (!(ok = la_wait_warp(&bar->mid, ph, abort))) break;
@@ -400,18 +417,19 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     for (int c = 0; c < chunks; ++c) {
       const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
       const int m = tokens(c);
-      if (!la_wait_warp(&bar->full_k[ph], ph2, abort)) break;
-      uint8_t* kb = sk + ph * SM::K;
+      const int st = stage(c);
+      if (!la_wait_warp(&bar->full_k[st], stage_ph(c), abort)) break;
+      uint8_t* kb = k_rows(st);
       if (m < LC) {
         // (a head has one such chunk, its last.)  Rows behind the sequence's end may hold
         // anything, NaN included, which a weight of zero does not remove: they are cleared
         // (before a sequence's start, where descending tiles end, TMA fills zeros)
-        if (!la_wait_warp(&bar->full_v[ph], ph2, abort)) break;
+        if (!la_wait_warp(&bar->full_v[st], stage_ph(c), abort)) break;
         if (!a.reverse) {
           for (int x = mt; x < (LC - m) * (DK / 8); x += LA_GROUP)
             *reinterpret_cast<uint4*>(kb + sw_off(m + x / (DK / 8), (x % (DK / 8)) * 8, LC)) = make_uint4(0u, 0u, 0u, 0u);
           for (int x = mt; x < (LC - m) * (DV / 8); x += LA_GROUP)
-            *reinterpret_cast<uint4*>(sv + ph * SM::V + sw_off(m + x / (DV / 8), (x % (DV / 8)) * 8, LC)) =
+            *reinterpret_cast<uint4*>(v_rows(st) + sw_off(m + x / (DV / 8), (x % (DV / 8)) * 8, LC)) =
                 make_uint4(0u, 0u, 0u, 0u);
         }
         // every warp has read the full chunks' weights before any passes the first barrier
@@ -486,7 +504,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       }
     }
   } else if (warp >= LA_ROLE_WARPS && warp < LA_ROLE_WARPS + 2 * LA_GROUP_WARPS) {
-    // ---------------- scores: P's pieces in place ----------------
+    // ---------------- scores: weighted, to bf16 in place ----------------
     regs_dec<LA_SCORE_REGS>();
     const int quad = warp & 3, hf = (warp - LA_ROLE_WARPS - LA_GROUP_WARPS) >> 2;
     const int row = quad * 32 + lane;               // TMEM lane: token row
@@ -571,7 +589,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const int mt = threadIdx.x - LA_ROLE_WARPS * 32 - 2 * LA_GROUP;
     auto st_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(LA_GROUP) : "memory"); };
 
-    // States in global memory go through the room of E's pieces when their rows are contiguous
+    // States in global memory go through the room of O's rows and of E when their rows are contiguous
     // (fp32 d x DV, 16-byte chunks swizzled by row: a thread's own row directly would touch 32
     // rows per access); transposed ones are contiguous across the lanes.
     constexpr int CH = DV / 4;
@@ -663,11 +681,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->ufree);
       if (local) continue;
-      if (c + 1 < chunks) {  // E's pieces, once Q E has read the ones before
+      if (c + 1 < chunks) {  // E in bf16, once Q E has read the one before
         if (!la_wait_warp(&bar->o1, ph, abort)) break;
         put_state(fast ? a_full : 1.f);
       }
-      // O leaves: through V's stage and TMA, or (partial chunk) straight to its rows
+      // O leaves: through shared memory and TMA, or (partial chunk) straight to its rows
       if (!la_wait_warp(&bar->o2[ph], (c >> 1) & 1, abort)) break;
       if (c > 0 && !la_wait_warp(&bar->store, ph ^ 1, abort)) break;  // the rows before have left
       tc_fence_after();
@@ -733,8 +751,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   __syncwarp();
   if (warp == 0 && lane == 0 && *abort) {
     // let the copies this CTA issued land before its shared memory goes away
-    for (int i = k_loads < 2 ? 0 : k_loads - 2; i < k_loads; ++i) drain_wait(&bar->full_k[i & 1], (i >> 1) & 1);
-    for (int i = v_loads < 2 ? 0 : v_loads - 2; i < v_loads; ++i) drain_wait(&bar->full_v[i & 1], (i >> 1) & 1);
+    for (int i = max(0, k_loads - stages); i < k_loads; ++i) drain_wait(&bar->full_k[stage(i)], stage_ph(i));
+    for (int i = max(0, v_loads - stages); i < v_loads; ++i) drain_wait(&bar->full_v[stage(i)], stage_ph(i));
     if (q_loads > 0) drain_wait(&bar->full_q, (q_loads - 1) & 1);
   }
   tc_fence_before();
@@ -804,8 +822,10 @@ int go_tc_shape(const TcPass& p, const CUtensorMap& q, const CUtensorMap& k, con
 
 }  // namespace
 
-// bf16, widths up to 128 in whole 16-byte vectors, rows on the 16-byte grid, and enough
-// tokens that a chunk of 128 is not mostly padding.
+// bf16, widths up to 128 in whole 16-byte vectors, rows on the 16-byte grid, and more tokens than
+// the kernel for a few of them takes: from 32 on the pass costs one chunk (8 heads of 64 x 64:
+// 8.4 us for 32 to 128 tokens, on the CUDA cores 14.5 for 32 and 48 for 128; 256 heads of
+// 128 x 128: 26 us against 35 for 32 tokens and 115 for 128).
 bool scan_tc_shape(const ScanArgs& a, int dtype) {
   return dtype == FWPKM_BF16 && a.d <= 128 && a.dv <= 128 && a.d % 8 == 0 && a.dv % 8 == 0 && a.T >= 32;
 }
@@ -813,8 +833,9 @@ bool scan_tc_takes(const ScanArgs& a, int dtype) {
   return scan_tc_shape(a, dtype) && grid16(a.q, a) && grid16(a.k, a) && grid16(a.v, a) && grid16(a.o, a);
 }
 
-// Segments: one when the heads fill half the GPU (a second wave or the extra pass over K and
-// V would cost more), else one CTA per SM, of at least two chunks each.
+// Segments: one when the heads fill half the GPU, else one CTA per SM, of at least two chunks
+// each.  (The extra pass over K and V costs half of the other: with two segments 74 heads of 8192
+// tokens take 216 us, 75 whole ones 243.)
 int scan_tc_segments(const ScanArgs& a) {
   const int heads = a.B * a.H;
   if (heads > 148 / 2) return 1;
