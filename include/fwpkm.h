@@ -432,7 +432,8 @@ fwpkm_status fwpkm_lookup_backward_workspace_size(const fwpkm_lookup_config* cfg
  *            (zero where nothing was read; also for n = 0); else the gradient is added to
  *            the rows that were read and the others are left as they were.
  *   dw       fp32 [n][R] or NULL; needs the table.
- *   table    read for dw only (else may be NULL).
+ *   table    read for dw only (else may be NULL); d_table may be the table itself (accumulate
+ *            with a negative scale: a step of gradient descent), dw is formed before.
  * The pairs are sorted by row, so each row's terms are summed in a fixed order.  The
  * workspace must not be shared with a call that may run at the same time. */
 fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* table, const void* idx, const float* w,
@@ -484,7 +485,8 @@ fwpkm_status fwpkm_balance_loss(const fwpkm_balance_config* cfg, const void* x, 
                                 float* usage, float* slope, void* stream);
 
 /* dx [groups][tokens][experts] (contiguous, the type of x) from the same x and mask, the
- * forward's slope and d_loss fp32 [groups] (NULL: ones). */
+ * forward's slope and d_loss fp32 [groups] (NULL: ones).  dx may be x's memory where x is
+ * contiguous. */
 fwpkm_status fwpkm_balance_loss_backward(const fwpkm_balance_config* cfg, const void* x, const uint8_t* mask,
                                          const float* slope, const float* d_loss, void* dx, void* stream);
 
@@ -515,7 +517,7 @@ typedef struct {
   int B, H;    /* sequences, heads per sequence                                    */
   int d, d_v;  /* widths of q, k and of v, o                                       */
   int dtype;   /* fwpkm_dtype of q, k, v, o and their gradients                    */
-  float scale; /* not 0                                                            */
+  float scale; /* finite and not 0, and so its reciprocal                          */
 } fwpkm_linattn_config;
 
 /* Bytes of device workspace (256-byte aligned, contents need not be initialised) of a call

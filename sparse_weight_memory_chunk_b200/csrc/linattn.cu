@@ -23,6 +23,7 @@
 // (194 a warp and token at d = d_v = 128, of them 64 packed FMAs): 256 heads of 512 tokens in
 // 350 us, 49 TFLOP/s.  (With rows staged by plain loads between two barriers the loads'
 // latency bounded it: 128 such heads in 665 us, now 232.)
+#include <cmath>
 #include <cstdio>
 #include <initializer_list>
 
@@ -556,7 +557,8 @@ int launch_scan(ScanArgs a, int dtype, int nseg, cudaStream_t s) {
 }
 
 fwpkm_status check_la(const fwpkm_linattn_config* c, int T) {
-  if (!c || c->B < 1 || c->H < 1 || c->d < 1 || c->d_v < 1 || T < 0 || !(c->scale == c->scale) || c->scale == 0.f)
+  if (!c || c->B < 1 || c->H < 1 || c->d < 1 || c->d_v < 1 || T < 0 || !std::isfinite(c->scale) ||
+      !std::isfinite(1.f / c->scale))  // (the gradients' descending passes run on states / scale)
     return FWPKM_ERR_INVALID_ARG;
   if (c->dtype != FWPKM_F32 && c->dtype != FWPKM_BF16) return FWPKM_ERR_INVALID_ARG;
   if (c->d > SC_MAX_D || c->d_v > SC_MAX_D || (long long)c->B * c->H > (1 << 24) || T > (1 << 28)) return FWPKM_ERR_UNSUPPORTED;

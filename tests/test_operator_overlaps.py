@@ -1,5 +1,6 @@
-"""Outputs of linear attention that begin where an input or another output does are refused on the
-host, before anything is enqueued (pointers are aligned numbers that nothing reads)."""
+"""Outputs of linear attention that begin where an input or another output does, and scales that
+have no finite reciprocal, are refused on the host, before anything is enqueued (pointers are
+aligned numbers that nothing reads)."""
 import ctypes as C
 
 import pytest
@@ -32,3 +33,13 @@ def test_outputs_in_the_memory_of_inputs_are_refused(lib):
             g[i] = other
             assert so.fwpkm_linear_attention_backward(cfg, q, k, v, T, fake, None, None, do, None, *g, None, work,
                                                       1 << 40, None) == -1
+
+
+@pytest.mark.parametrize("scale", [0.0, float("inf"), -float("inf"), float("nan"), 1e-39])
+def test_scales_without_a_reciprocal_are_refused(lib, scale):
+    so = lib.lib()
+    cfg = C.byref(lib.LinattnConfig(2, 2, 32, 32, lib.F32, scale))
+    fake, work = C.c_void_p(1 << 20), C.c_void_p(1 << 30)
+    q, k, v, o = (C.byref(lib.Heads((i + 2) << 24, 1 << 16, 1 << 12, 64)) for i in range(4))
+    assert so.fwpkm_linear_attention(cfg, q, k, v, 10, fake, None, None, o, None, work, 1 << 40, None) == -1
+    assert so.fwpkm_linear_attention_step(cfg, q, k, v, 1, fake, None, fake, o, fake, None) == -1
