@@ -314,8 +314,7 @@ def _call(t, stream, where, fn, *args):
     else:
         _need(stream.device_index == dev, "the stream is another device's than the tensors")
         handle = stream.cuda_stream
-    cur = torch.cuda.current_device()
-    if cur == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -351,8 +350,8 @@ def _scratch(workspace, nbytes, like, stream, what):
         import torch
         workspace = _empty(stream, nbytes, torch.uint8, like)
         return workspace, workspace.data_ptr(), nbytes
-    _need(workspace.device == like.device and workspace.is_contiguous(),
-          f"{what}: the workspace must be contiguous, on {like.device}")
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"{what}: the workspace must be contiguous, on {like.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -445,7 +444,8 @@ def _balance_config(x, idx, mask, kind, coef):
     import torch
     _need(x.dim() == 3 and (x.stride(2) == 1 or x.shape[2] <= 1),
           "x must be [groups][tokens][experts], its rows contiguous")
-    _need(kind in BALANCE_KIND, f"kind must be one of {sorted(BALANCE_KIND)}")
+    if kind not in BALANCE_KIND:
+        raise ValueError(f"kind must be one of {sorted(BALANCE_KIND)}")
     G, T, E = x.shape
     k = 0
     if idx is not None:
@@ -471,13 +471,12 @@ def balance_loss(x, idx=None, mask=None, kind="load", coef=1.0, workspace=None, 
                             _bytes(L.fwpkm_balance_workspace_size, "balance_loss", c), x, stream, "balance_loss")
     r = BalanceLoss()
     r.kind, r.coef = kind, coef
-    f = _empty(stream, 2 * G * E + G, torch.float32, x)
-    r.usage, r.slope, r.loss = f[:G * E].view(G, E), f[G * E:2 * G * E].view(G, E), f[2 * G * E:]
+    r.loss = _empty(stream, G, torch.float32, x)
+    r.usage, r.slope = _empty(stream, (G, E), torch.float32, x), _empty(stream, (G, E), torch.float32, x)
     r.counts = None if idx is None else _empty(stream, (G, E), torch.int32, x)
-    p = f.data_ptr()
     _call(x, stream, "balance_loss", L.fwpkm_balance_loss, c, x.data_ptr(), None if idx is None else idx.data_ptr(),
-          None if mask is None else mask.data_ptr(), pw, nw, p + 8 * G * E, None if idx is None else r.counts.data_ptr(),
-          p, p + 4 * G * E)
+          None if mask is None else mask.data_ptr(), pw, nw, r.loss.data_ptr(),
+          None if idx is None else r.counts.data_ptr(), r.usage.data_ptr(), r.slope.data_ptr())
     return r
 
 
@@ -498,10 +497,10 @@ def balance_loss_backward(x, result: BalanceLoss, mask=None, d_loss=None, dx=Non
     return dx
 
 
-def _heads(t, like, shape, what):
+def _heads(t, dtype, device, shape, what):
     """A [B][H][T][w] tensor of any strides with contiguous rows."""
-    if t.shape != shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{what} must be a {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
     sb, sh, st, se = t.stride()
     if se != 1 and shape[3] > 1:
         raise ValueError(f"{what}: the rows must be contiguous")
@@ -511,14 +510,15 @@ def _heads(t, like, shape, what):
 def _linattn_args(q, k, v, log_decay, scale, lens):
     import torch
     _need(q.dim() == 4 and v.dim() == 4, "q, k, v must be [B][H][T][width]")
-    qs = q.shape
+    _need(log_decay is not None, "log_decay is needed")
+    qs, dt, dev = q.shape, q.dtype, q.device
     B, H, T, d = qs
     dv = v.shape[3]
-    hq, hk, hv = _heads(q, q, qs, "q"), _heads(k, q, qs, "k"), _heads(v, q, (B, H, T, dv), "v")
-    _need(log_decay is not None, "log_decay is needed")
+    like = dt, dev
+    hq, hk, hv = _heads(q, dt, dev, qs, "q"), _heads(k, dt, dev, qs, "k"), _heads(v, dt, dev, (B, H, T, dv), "v")
     ld = _side(log_decay, q, torch.float32, (H,), "log_decay")
-    ln = _side(lens, q, torch.int32, (B,), "lens")
-    return ctypes.byref(LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale)), hq, hk, hv, ld, ln, B, H, T, d, dv
+    ln = None if lens is None else _side(lens, q, torch.int32, (B,), "lens")
+    return ctypes.byref(LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale)), hq, hk, hv, ld, ln, B, H, T, d, dv, like
 
 
 def _rows_like(t, B, H, T, w, stream):
@@ -539,10 +539,10 @@ def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, 
     [B] int32.  sT is None unless given or asked for with final_state.  Rows of o behind a
     sequence's end are left as they were (a new o holds anything there)."""
     import torch
-    c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
+    c, hq, hk, hv, ld, ln, B, H, T, d, dv, like = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
         o = _rows_like(v, B, H, T, dv, stream)
-    ho = _heads(o, q, (B, H, T, dv), "o")
+    ho = _heads(o, *like, (B, H, T, dv), "o")
     if sT is None and final_state:
         sT = _empty(stream, (B, H, d, dv), torch.float32, q)
     p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
@@ -561,11 +561,11 @@ def linear_attention_backward(q, k, v, log_decay, d_o, scale=1.0, s0=None, d_sT=
     final state's gradient d_sT (None: zero).  `grads`: (dq, dk, dv) to fill; ds0 is None with
     state_grad=False.  Rows behind a sequence's end are left as they were."""
     import torch
-    c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
-    ho = _heads(d_o, q, (B, H, T, dv), "d_o")
+    c, hq, hk, hv, ld, ln, B, H, T, d, dv, like = _linattn_args(q, k, v, log_decay, scale, lens)
+    ho = _heads(d_o, *like, (B, H, T, dv), "d_o")
     if grads is None:
         grads = tuple(_rows_like(q, B, H, T, w, stream) for w in (d, d, dv))
-    hg = [_heads(t, q, (B, H, T, w), n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
+    hg = [_heads(t, *like, (B, H, T, w), n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
     if ds0 is None and state_grad:
         ds0 = _empty(stream, (B, H, d, dv), torch.float32, q)
     p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
@@ -586,10 +586,10 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
     states [B][H][d][d_v], which are updated in place unless state_out is given or
     in_place=False (then a new tensor is)."""
     import torch
-    c, hq, hk, hv, ld, ln, B, H, T, d, dv = _linattn_args(q, k, v, log_decay, scale, lens)
+    c, hq, hk, hv, ld, ln, B, H, T, d, dv, like = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
         o = _rows_like(v, B, H, T, dv, stream)
-    ho = _heads(o, q, (B, H, T, dv), "o")
+    ho = _heads(o, *like, (B, H, T, dv), "o")
     _need(state is not None, "state is needed")
     ps = _side(state, q, torch.float32, (B, H, d, dv), "state")
     if state_out is None:
