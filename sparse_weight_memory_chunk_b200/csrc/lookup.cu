@@ -493,12 +493,13 @@ sort_cluster_kernel(const I* __restrict__ idx, int P, long long rows, int per, i
 
 // ---------------------------------------------------------------------------
 // Segmented sum of the sorted pairs.  A team of tx_n threads (one vector of columns each)
-// owns SEG consecutive sorted pairs.  A row whose pairs lie inside the range is written at
+// owns `seg` consecutive sorted pairs.  A row whose pairs lie inside the range is written at
 // once; a row cut by the range's ends leaves a partial sum, and the second launch adds a
-// cut row's partials in order.  SEG = 32 bounds the serial work on a row that everything
-// reads to SEG terms plus its partials.
+// cut row's partials in order.  The serial work on a row that everything reads is seg terms
+// plus its partials: short ranges for few pairs (1761 pairs of 240 rows of 512 fp32, sums and
+// join: 19 us with 32, 15 with 16), long ones for many (32768 pairs of 100 rows: 33 and 42).
 // ---------------------------------------------------------------------------
-constexpr int SEG = 32;
+int seg_pairs(long long P) { return P <= 2048 ? 8 : P <= 8192 ? 16 : 32; }
 constexpr int ZERO_BYTES = 8192;
 
 struct SegArgs {
@@ -507,7 +508,7 @@ struct SegArgs {
   long long P, rows, out_ld, grad_ld;
   int R, vecs, tx_n, width;
   float scale;
-  int accumulate;
+  int accumulate, seg;
   float* part;        // [ranges][2][width] fp32: the sums cut at the range's start and end
   long long ranges;
 };
@@ -643,7 +644,7 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
   const int c = blockIdx.y * a.tx_n + tx;
   const long long range = (long long)blockIdx.x * ty_n + ty;
   if (c >= a.vecs || range >= a.ranges) return;
-  const long long p0 = range * SEG, p1 = p0 + SEG < a.P ? p0 + SEG : a.P;
+  const long long p0 = range * a.seg, p1 = p0 + a.seg < a.P ? p0 + a.seg : a.P;
   constexpr int SEG_U = ACC && VEC == 8 ? 4 : 8;
   const uint32_t none = (uint32_t)a.rows;
   float acc[VEC];
@@ -670,12 +671,14 @@ lookup_sum_kernel(SegArgs a, const T* __restrict__ d_out, G* __restrict__ d_tabl
     GRow<G, VEC> old[SEG_U];
 #pragma unroll
     for (int u = 0; u < SEG_U; ++u) {
+      // (in vectors also for a pair that is none, so that the loads go out together: 5000 pairs of
+      // 1000 bf16 30 -> 21 us; by elements that took 102 us instead of 86 for 16000 pairs of 1291)
       f[u] = 0.f;
-      if (k[u] != none) {
+      if (VEC > 1 || k[u] != none) {
         f[u] = a.w ? __ldg(a.w + pr[u]) : 1.f;
         x[u] = *reinterpret_cast<const Pack<T, VEC>*>(d_out + (long long)(pr[u] / a.R) * a.out_ld + (long long)c * VEC);
         // the row's last pair here: what the gradient is added to, loaded with the pairs
-        if (ACC && k[u] != (u + 1 < SEG_U ? k[(u + 1) % SEG_U] : after)) old[u].load(d_table, a, k[u], c);
+        if (ACC && k[u] != none && k[u] != (u + 1 < SEG_U ? k[(u + 1) % SEG_U] : after)) old[u].load(d_table, a, k[u], c);
       }
     }
 #pragma unroll
@@ -723,7 +726,7 @@ lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
   const int c = blockIdx.y * a.tx_n + tx;
   const long long range = (long long)blockIdx.x * ty_n + ty;
   if (c >= a.vecs || range + 1 >= a.ranges) return;
-  const long long p0 = range * SEG, p1 = p0 + SEG;  // not the last range: full
+  const long long p0 = range * a.seg, p1 = p0 + a.seg;  // not the last range: full
   const uint32_t row = a.item[p1 - 1].x;
   if (row == (uint32_t)a.rows || a.item[p1].x != row) return;     // nothing cut at the end
   if (a.item[p0].x == row && p0 > 0 && a.item[p0 - 1].x == row) return;  // the row began earlier
@@ -731,7 +734,7 @@ lookup_join_kernel(SegArgs a, G* __restrict__ d_table) {
   long long lo = range + 1, hi = a.ranges;
   while (lo < hi) {
     const long long mid = (lo + hi) >> 1;
-    if (a.item[mid * SEG].x == row) lo = mid + 1;
+    if (a.item[mid * a.seg].x == row) lo = mid + 1;
     else hi = mid;
   }
   float acc[VEC];
@@ -784,7 +787,8 @@ struct BackWork {
 };
 size_t back_carve(const fwpkm_lookup_config& c, long long P, char* base, BackWork* w) {
   const SortPlan sp = sort_plan(c.rows, P);
-  const long long ranges = (P + SEG - 1) / SEG;
+  const int seg = seg_pairs(P);
+  const long long ranges = (P + seg - 1) / seg;
   size_t off = 0;
   auto take = [&](size_t bytes) -> char* {
     char* p = base ? base + off : nullptr;
@@ -1117,7 +1121,8 @@ fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* t
     a.P = P;
     a.rows = cfg->rows; a.out_ld = cfg->out_ld; a.grad_ld = grad_ld;
     a.R = cfg->R; a.width = cfg->width; a.scale = cfg->scale; a.accumulate = accumulate != 0;
-    a.ranges = (P + SEG - 1) / SEG;
+    a.seg = seg_pairs(P);
+    a.ranges = (P + a.seg - 1) / a.seg;
     a.w = w;
     a.item = bw.item[at];
     a.part = bw.part;
