@@ -80,43 +80,41 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const char* src, int byte
   }
 }
 
-// N values in a row of shared memory (N * sizeof(T) a multiple of 16, or N <= 4).
+// N (even) values in a row of shared memory, which start on a grid of N.
 template <int N>
 __device__ __forceinline__ void get_row(const float* p, float (&x)[N]) {
-  if (N % 4 == 0) {
+  constexpr int V = N % 4 == 0 ? 4 : 2;  // values per load
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
+  for (int i = 0; i < N; i += V) {
+    if (V == 4) {
       const float4 y = *reinterpret_cast<const float4*>(p + i);
-      x[i] = y.x; x[(i + 1) % N] = y.y; x[(i + 2) % N] = y.z; x[(i + 3) % N] = y.w;
+      x[i] = y.x; x[i + 1] = y.y; x[(i + 2) % N] = y.z; x[(i + 3) % N] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(p + i);
+      x[i] = y.x; x[i + 1] = y.y;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = p[i];
   }
 }
 template <int N>
 __device__ __forceinline__ void get_row(const __nv_bfloat16* p, float (&x)[N]) {
-  if (N % 4 == 0) {
-    constexpr int V = N % 8 == 0 ? 4 : 2;  // words per load
+  constexpr int V = N % 8 == 0 ? 4 : N % 4 == 0 ? 2 : 1;  // words per load
 #pragma unroll
-    for (int i = 0; i < N; i += 2 * V) {
-      uint32_t w[4];
-      if (V == 4) {
-        const uint4 y = *reinterpret_cast<const uint4*>(p + i);
-        w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
-      } else {
-        const uint2 y = *reinterpret_cast<const uint2*>(p + i);
-        w[0] = y.x; w[1] = y.y;
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[(i + 2 * j) % N] = __uint_as_float(w[j] << 16);
-        x[(i + 2 * j + 1) % N] = __uint_as_float(w[j] & 0xffff0000u);
-      }
+  for (int i = 0; i < N; i += 2 * V) {
+    uint32_t w[4];
+    if (V == 4) {
+      const uint4 y = *reinterpret_cast<const uint4*>(p + i);
+      w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
+    } else if (V == 2) {
+      const uint2 y = *reinterpret_cast<const uint2*>(p + i);
+      w[0] = y.x; w[1] = y.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p + i);
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __bfloat162float(p[i]);
+    for (int j = 0; j < V; ++j) {
+      x[(i + 2 * j) % N] = __uint_as_float(w[j] << 16);
+      x[(i + 2 * j + 1) % N] = __uint_as_float(w[j] & 0xffff0000u);
+    }
   }
 }
 
@@ -458,9 +456,9 @@ ScanShape scan_shape(const ScanArgs& a) {
     return base * (n < 1 ? 1 : n);
   };
   auto rows = [&](int l) {
-    int ni = 2;
-    while (ni * (SC_THREADS / l) < a.d) ni <<= 1;
-    return ni;
+    for (int ni : {2, 4, 6, 8, 12})
+      if (ni * (SC_THREADS / l) >= a.d) return ni;
+    return 16;
   };
   while (lj > 4 && ctas(lj) <= (rows(lj) > 4 ? 150 : 75) && 2 * ctas(lj / 2) >= 3 * ctas(lj)) lj >>= 1;
   const int ni = rows(lj);
@@ -504,7 +502,9 @@ int go_scan(const ScanArgs& a, int local, cudaStream_t s) {
   switch (sh.ni) {
     FWPKM_SCAN(2)
     FWPKM_SCAN(4)
+    FWPKM_SCAN(6)
     FWPKM_SCAN(8)
+    FWPKM_SCAN(12)
     FWPKM_SCAN(16)
     default: return -1;
   }
