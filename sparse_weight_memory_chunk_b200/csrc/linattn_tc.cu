@@ -34,7 +34,7 @@
 //   keys          K hi(c)              K pieces(c+1)
 //   scores                        P bf16(c)
 //   state   O out(c-1)                 E(c)      E bf16(c+1)
-// so the MMAs of a chunk (6 products of 128^3, 3072 cycles at the dense rate; 5 where no state
+// so the MMAs of a chunk (6 products of 128^3, 512 cycles each at the dense rate; 5 where no state
 // leaves) follow one another while the groups work beside them.  (With the groups' steps done in
 // turn by the same warps a chunk took the sum of their latencies, 5.5 us of 148 heads at
 // d = d_v = 128.)  A pass that only forms segment states has TMEM to spare and keeps two sets of
