@@ -499,9 +499,9 @@ fwpkm_status fwpkm_balance_loss_backward(const fwpkm_balance_config* cfg, const 
  * gets no gradient.  States are fp32 [B][H][d][d_v], contiguous; q, k, v, o and their
  * gradients fp32 or bf16 (cfg.dtype).  Sums and states are held in fp32.  bf16 prompts run on
  * the tensor cores in chunks of 128 tokens: the weighted scores q.k inside a chunk and the
- * state before it enter o's products rounded once to bf16 (half a step, 2^-9 of a term on
- * average, beside o's own rounding), the keys in the state as two bf16 pieces, and as three
- * where the state leaves (sT, ds0: fp32 arithmetic).  A value that is not finite makes what
+ * state before it enter o's products as two bf16 pieces (2^-16 of a term left out, where o's own
+ * rounding is 2^-8), the keys in the state likewise, and as three pieces where the state leaves
+ * (sT, ds0: fp32 arithmetic).  A value that is not finite makes what
  * depends on it not finite, and there also the earlier rows of its chunk.
  * ------------------------------------------------------------------------- */
 

@@ -13,36 +13,34 @@
 // as a^128 E, and R_t multiplies the finished row of O.  A head whose a^128 is out of range
 // (|log a^128| > LA_RANGE) takes the weights element by element and scales Q E in place.
 //
-// Precision: the inputs are bf16, exact operands.  P (weighted) and E enter their product
-// rounded to bf16 once, as O is on its way out: every term of O passes through one of the two,
-// so O is sqrt(2) bf16 roundings off fp32 arithmetic (measured 2.3e-3 of its norm against
-// 1.65e-3; with both as two pieces 1.65e-3, and a chunk 0.6 us longer).  What reaches the state
-// is not rounded: the weighted keys of U as hi + mid + lo where the state is handed on in fp32 (exact to fp32),
-// else as two (2^-17 left out).  U adds the small pieces first, so few of the accumulator's roundings (which
+// Precision: the inputs are bf16, exact operands.  P (weighted) and E enter their products as two
+// bf16 pieces, the upper half of the float and what that leaves (2^-16 left out at most), so O is off by
+// its own rounding on the way out (1.66e-3 of its norm; rounded once each, P and E made it 2.35e-3, and a
+// chunk 0.5 us shorter).  The weighted keys of U are hi + mid + lo where the state is handed on in fp32 (exact to fp32),
+// else two pieces.  U adds the small pieces first, so few of the accumulator's roundings (which
 // truncate) are at full size: the state is 9e-8 off against 6e-7 the other way round.  E is
 // kept in fp32 registers and U is a fresh accumulator per chunk, so the tensor cores' running
 // sums span one chunk only.
 //
 // CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one, the
-// rows of O through shared memory; a pass that only forms segment states: K, V three stages), warp 1 owns TMEM and issues the MMAs (one thread),
+// rows of O from the room of the chunk's V; a pass that only forms segment states: K, V three stages), warp 1 owns TMEM and issues the MMAs (one thread),
 // warps 4-11 weight the keys, 12-19 the scores, 20-27 carry the state and the output: a warp
 // reads TMEM lanes 32 (w % 4).. and one half of the columns.  TMEM (512 columns): P fp32,
-// overwritten in place by its bf16 pairs (operand A of P V); O; U; two pieces of the
+// overwritten in place by its pieces' bf16 pairs (operand A of P V); O; U; two pieces of the
 // weighted, transposed keys (operand A of U; the high piece waits in registers and takes the
 // low one's place).  Per chunk c, in order:
-//   MMA     U lo, mid(c)   P(c)   U hi(c)        Q E(c)               P V(c)
+//   MMA     U lo, mid(c)   P(c)   U hi(c)        Q E lo, hi(c)        P V lo, hi(c)
 //   keys          K hi(c)              K pieces(c+1)
-//   scores                        P bf16(c)
-//   state   O out(c-1)                 E(c)      E bf16(c+1)
-// so the MMAs of a chunk (6 products of 128^3, 512 cycles each at the dense rate; 5 where no state
+//   scores                        P pieces(c)
+//   state   O out(c-1)                 E(c)      E pieces(c+1)
+// so the MMAs of a chunk (8 products of 128^3, 512 cycles each at the dense rate; 7 where no state
 // leaves) follow one another while the groups work beside them.  (With the groups' steps done in
 // turn by the same warps a chunk took the sum of their latencies, 5.5 us of 148 heads at
 // d = d_v = 128.)  A pass that only forms segment states has TMEM to spare and keeps two sets of
 // key pieces, so that weighting a chunk's keys overlaps the products of the one before.
 // Bound: for d = d_v = 128 a chunk is 128 KB, 3.0 us of an SM's share of the copy bandwidth; 148
-// heads of 8192 tokens take 4.2 us a chunk (72% of it), 4.5 with the final state (tensor pipe 38%
-// active, issue slots 50%): what is left is the chain state -> E bf16 -> Q E -> next state, and
-// keys -> U -> next keys.
+// heads of 8192 tokens take 4.7 us a chunk (64% of it), 5.0 with the final state: what is left is
+// the chain state -> E pieces -> Q E -> next state, and keys -> U -> next keys.
 #include <cstdio>
 
 #include "linattn.cuh"
@@ -74,16 +72,17 @@ constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_K0 = 384, TM_COLS = 512;
 
 struct TcBars {
   uint64_t full_q, full_k[3], full_v[3], free_k[3], o2[2], kt[2], u2[2];
-  uint64_t p, o1, staged, khi, u1, mid, est, ofree, ufree, cleared, store, drain, stall;
+  uint64_t p, o1, staged, khi, u1, mid, est, ofree, ufree, cleared, drain, stall;
 };
 
 template <int DK, int DV>
 struct TcSmem {
   static constexpr int Q = LC * DK * 2, K = LC * DK * 2, V = LC * DV * 2, E = DK * DV * 2;
-  static constexpr int off_k = Q, off_v = off_k + 2 * K, off_o = off_v + 2 * V, off_e = off_o + V;
-  // states pass through O's rows and E's room (V + E >= DK * DV * 4 for V = 128 rows)
+  // E's two pieces; in between, states pass through their room in fp32.  (The low one's place is as
+  // large as a stage of V, whose third it is where only states are formed.)
+  static constexpr int off_k = Q, off_v = off_k + 2 * K, off_elo = off_v + 2 * V, off_e = off_elo + V;
   static constexpr int off_tab = off_e + E;
-  static_assert(V + E >= DK * DV * 4, "room for a state in fp32");
+  static_assert(V >= E && V + E >= DK * DV * 4, "room for a state in fp32");
   static constexpr int need = off_tab + 4 * (3 * LC + 4) + (int)sizeof(TcBars) + 16 + 1024;
   // one CTA per SM: each holds all of TMEM
   static constexpr int bytes = need > 120 * 1024 ? need : 120 * 1024;
@@ -163,7 +162,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   using SM = TcSmem<DK, DV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sq = smem, *sk = smem + SM::off_k, *sv = smem + SM::off_v, *so = smem + SM::off_o, *se = smem + SM::off_e;
+  uint8_t *sq = smem, *sk = smem + SM::off_k, *sv = smem + SM::off_v, *selo = smem + SM::off_elo, *se = smem + SM::off_e;
   float* bw = (float*)(smem + SM::off_tab);  // [LC] column weights B_s
   float* kw = bw + LC;                       // [LC] weights of the chunk's keys
   float* pw = kw + LC;                       // [LC + 1] a^j
@@ -201,7 +200,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     mbar_init(&bar->ufree, LA_GROUP_WARPS);
     mbar_init(&bar->cleared, LA_GROUP_WARPS);
     mbar_init(&bar->staged, LA_GROUP_WARPS);
-    mbar_init(&bar->store, 1);
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
     *abort = 0;
@@ -242,12 +240,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   auto tile_t = [&](int c) { return a.reverse ? n - (t0 + c * LC) - LC : t0 + c * LC; };
   auto tokens = [&](int c) { return min(LC, t1 - t0 - c * LC); };
 
-  // K and V: two stages, and where only states are formed a third in the room of Q and of O
+  // K and V: two stages, and where only states are formed a third in the room of Q and of E's low piece
   const int stages = local ? 3 : 2;
   auto stage = [&](int c) { return local ? c % 3 : c & 1; };
   auto stage_ph = [&](int c) { return (uint32_t)((local ? c / 3 : c >> 1) & 1); };
   auto k_rows = [&](int st) { return st == 2 ? sq : sk + st * SM::K; };
-  auto v_rows = [&](int st) { return st == 2 ? so : sv + st * SM::V; };
+  auto v_rows = [&](int st) { return st == 2 ? selo : sv + st * SM::V; };
 
   int k_loads = 0, v_loads = 0, q_loads = 0;  // producer: chunks whose loads were issued
   if (warp < LA_ROLE_WARPS) regs_dec<LA_ROLE_REGS>();
@@ -282,7 +280,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         load_v(c);
       }
       for (int c = 0; c < chunks; ++c) {
-        const uint32_t ph = (c >> 1) & 1;
         if (!la_wait(&bar->free_k[stage(c)], stage_ph(c), abort)) break;
         load_k(c + stages);
         if (local) {
@@ -291,16 +288,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
         if (!la_wait(&bar->o1, c & 1, abort)) break;
         load_q(c + 1);
-        if (!la_wait(&bar->o2[c & 1], ph, abort)) break;
-        load_v(c + 2);
+        // O's rows lie in the chunk's stage of V, which is loaded again once they have left
         if (!la_wait(&bar->staged, c & 1, abort)) break;
-        if (tokens(c) == LC) {  // (the rows of a partial chunk are written by the state warps)
+        if (tokens(c) == LC) {  // (the rows of a partial chunk, the last, are written by the state warps)
           for (int x = 0; x < DV; x += 64)
-            tma_store_4d(&mo, so + (x >> 6) * LA_BLOCK, x, tile_t(c), h * ps.co.h, b * ps.co.b);
+            tma_store_4d(&mo, v_rows(stage(c)) + (x >> 6) * LA_BLOCK, x, tile_t(c), h * ps.co.h, b * ps.co.b);
           bulk_commit();
           bulk_wait_read();
         }
-        mbar_arrive(&bar->store);  // O's rows may be overwritten
+        load_v(c + 2);
       }
       bulk_wait_all();
     }
@@ -308,7 +304,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (chunks > 0) {
       // ---------------- MMA issuer: the warp waits together, one lane issues ----------------
       constexpr uint32_t id_p = idesc_bf16_f32(LC, LC), id_v = idesc_bf16_f32(LC, DV) | IDESC_B_MN;
-      const uint32_t q0 = smem_u32(sq), e0 = smem_u32(se);
+      const uint32_t q0 = smem_u32(sq), e0 = smem_u32(se), elo0 = smem_u32(selo);
       bool ok = !(ps.stall && !la_wait_warp(&bar->stall, 0, abort));
       for (int c = 0; c < chunks && ok; ++c) {
         const uint32_t ph = c & 1, ph2 = (c >> 1) & 1;
@@ -373,11 +369,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         tc_fence_after();
         if (elect_one()) {
           if (state) {
-            const uint64_t qd = sdesc_k_sw128(q0), ed = sdesc_mn_sw128(e0, DK * 128);
+            const uint64_t qd = sdesc_k_sw128(q0);
+#pragma unroll
+            for (int piece = 0; piece < 2; ++piece) {
+              const uint64_t ed = sdesc_mn_sw128(piece == 0 ? elo0 : e0, DK * 128);
 #pragma unroll 2
-            for (int kk = 0; kk < DK / 16; ++kk)
-              umma_bf16(tmem + TM_O, qd + (kk >> 2) * (LA_BLOCK >> 4) + (kk & 3) * 2, ed + kk * 128, id_v,
-                        kk != 0 ? 1u : 0u);
+              for (int kk = 0; kk < DK / 16; ++kk)
+                umma_bf16(tmem + TM_O, qd + (kk >> 2) * (LA_BLOCK >> 4) + (kk & 3) * 2, ed + kk * 128, id_v,
+                          (piece | kk) != 0 ? 1u : 0u);
+            }
           }
           umma_commit(&bar->o1);  // also: Q and E have been read
         }
@@ -385,10 +385,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (!(ok = la_wait_warp(&bar->mid, ph, abort))) break;
         tc_fence_after();
         if (elect_one()) {
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece)
 #pragma unroll 2
-          for (int kk = 0; kk < LC / 16; ++kk)  // (P's bf16 columns: the first 16 of every 32)
-            umma_bf16_ta(tmem + TM_O, tmem + TM_P + (kk >> 1) * 32 + (kk & 1) * 8, vd + kk * 128, id_v,
-                         (state || kk != 0) ? 1u : 0u);
+            for (int kk = 0; kk < LC / 16; ++kk)  // (of every 32 columns of P, 16 of high and 16 of low pieces)
+              umma_bf16_ta(tmem + TM_O, tmem + TM_P + (kk >> 1) * 32 + (1 - piece) * 16 + (kk & 1) * 8, vd + kk * 128,
+                           id_v, (state || (piece | kk) != 0) ? 1u : 0u);
           umma_commit(&bar->o2[ph]);
         }
         __syncwarp();
@@ -522,14 +524,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       // a warp's two 32 x 32 blocks are behind the tokens, ahead of them (zero), or on the
       // diagonal; the halves interleave the blocks, so that their work is even
 #pragma unroll 1
-      for (int blk = hf; blk < 4; blk += 2) {       // 32 columns become 16 of bf16 pairs
+      for (int blk = hf; blk < 4; blk += 2) {       // 32 columns become 16 of high and 16 of low pairs
         const int dq = a.reverse ? blk - quad : quad - blk, s0 = blk * 32;
-        uint32_t y[16];
+        uint32_t v[32];
         if (dq < 0) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = 0u;
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
         } else {
-          uint32_t v[32];
           tmem_ld32(lanes + TM_P + s0, v);
           tmem_wait_ld();
           if (!fast) {
@@ -544,6 +545,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             for (int i = 0; i < 32; ++i)
               if (a.reverse ? i < lane : i > lane) v[i] = 0u;
           }
+          uint32_t lo[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float4 w = *reinterpret_cast<const float4*>(bw + s0 + 4 * i);
@@ -551,11 +553,17 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             float x2 = __uint_as_float(v[4 * i + 2]), x3 = __uint_as_float(v[4 * i + 3]);
             mul2(x0, x1, w.x, w.y);
             mul2(x2, x3, w.z, w.w);
-            y[2 * i] = pack_bf16(x0, x1);
-            y[2 * i + 1] = pack_bf16(x2, x3);
+            v[2 * i] = pack_high(x0, x1);
+            v[2 * i + 1] = pack_high(x2, x3);
+            below_high(v[2 * i], x0, x1);
+            below_high(v[2 * i + 1], x2, x3);
+            lo[2 * i] = pack_bf16(x0, x1);
+            lo[2 * i + 1] = pack_bf16(x2, x3);
           }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[16 + i] = lo[i];
         }
-        tmem_st16(lanes + TM_P + s0, y);
+        tmem_st32(lanes + TM_P + s0, v);
       }
       if (!fast && (init != nullptr || c > 0)) {
         // O = Q E so far: decay each token's row
@@ -589,11 +597,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const int mt = threadIdx.x - LA_ROLE_WARPS * 32 - 2 * LA_GROUP;
     auto st_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(LA_GROUP) : "memory"); };
 
-    // States in global memory go through the room of O's rows and of E when their rows are contiguous
+    // States in global memory go through the room of E's pieces when their rows are contiguous
     // (fp32 d x DV, 16-byte chunks swizzled by row: a thread's own row directly would touch 32
     // rows per access); transposed ones are contiguous across the lanes.
     constexpr int CH = DV / 4;
-    auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(so + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
+    auto chunk_at = [&](int r, int ch) { return reinterpret_cast<float4*>(selo + r * DV * 4 + ((ch ^ (r & (CH - 1))) << 4)); };
     float S[EC];
     if (init) {
       if (isj == 1 && (a.dv & 3) == 0 && ((uintptr_t)init & 15) == 0 && (isi & 3) == 0) {
@@ -630,18 +638,22 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
       for (int j = 0; j < EC; ++j) S[j] = 0.f;
     }
-    auto put_state = [&](float f) {  // f E in bf16, the second operand of Q E
+    auto put_state = [&](float f) {  // f E in two bf16 pieces, the second operand of Q E
       if (row < DK) {
 #pragma unroll
         for (int j = 0; j < EC; j += 8) {
-          uint32_t y[4];
+          uint32_t y[4], lo[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float x0 = S[j + 2 * u], x1 = S[j + 2 * u + 1];
             mul2(x0, x1, f, f);
-            y[u] = pack_bf16(x0, x1);
+            y[u] = pack_high(x0, x1);
+            below_high(y[u], x0, x1);
+            lo[u] = pack_bf16(x0, x1);
           }
-          *reinterpret_cast<uint4*>(se + sw_off(row, j0 + j, DK)) = make_uint4(y[0], y[1], y[2], y[3]);
+          const uint32_t at = sw_off(row, j0 + j, DK);
+          *reinterpret_cast<uint4*>(se + at) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(selo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_async_smem();
@@ -685,10 +697,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (!la_wait_warp(&bar->o1, ph, abort)) break;
         put_state(fast ? a_full : 1.f);
       }
-      // O leaves: through shared memory and TMA, or (partial chunk) straight to its rows
+      // O leaves: through the room of the chunk's V, which P V was the last to read, and TMA, or
+      // (partial chunk) straight to its rows
       if (!la_wait_warp(&bar->o2[ph], (c >> 1) & 1, abort)) break;
-      if (c > 0 && !la_wait_warp(&bar->store, ph ^ 1, abort)) break;  // the rows before have left
       tc_fence_after();
+      uint8_t* so = v_rows(stage(c));
       const int r0 = a.reverse ? LC - m : 0;
 #pragma unroll 1
       for (int q = 0; q < EC; q += 16) {
@@ -727,8 +740,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const long long osi = local ? a.dv : a.si, osj = local ? 1 : a.sj;
       const float w = local || n == 0 ? 1.f : a.st_scale * (a.out_decay ? decay_pow(ld, 1.f) : 1.f);
       if (osj == 1 && (a.dv & 3) == 0 && ((uintptr_t)dst & 15) == 0 && (osi & 3) == 0) {
-        // (the last chunk's O was waited for, so Q E has read E; its rows have to have left)
-        if (!local && chunks > 0) la_wait_warp(&bar->store, (chunks - 1) & 1, abort);
+        // (the last chunk's O was waited for, so Q E has read E; where only states are formed, its last U
+        // was, which reads the third stage of V)
         if (row < a.d) {
 #pragma unroll
           for (int j = 0; j < EC; j += 4)

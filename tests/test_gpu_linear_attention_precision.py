@@ -1,0 +1,62 @@
+"""Linear attention of bf16 prompts is off by its outputs' own rounding and fp32 arithmetic, no more.
+
+Tolerances (u = 2^-24, h = 2^-8, A the same sums over absolute values).  fp32 arithmetic is off by
+c u A, c = T + d + d_v + 32 (the roundings that a term passes through).  On the tensor cores a
+weighted score, or the state before a chunk, enters o as two bf16 pieces: the high one leaves less
+than 2^-7 of it, the low one is off by half a step of that, 2^-16; the keys in that state likewise.
+2^-16 A + 2^-16 A is 2^9 u A.  The bf16 result adds h of itself.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from sparse_weight_memory_chunk_b200 import fwpkm  # noqa: E402
+
+from oracle import operators as op  # noqa: E402
+
+U, HB = 2.0 ** -24, 2.0 ** -8
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def rand(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def close(got, ref, size, c, what):
+    tol = c * U * size + 1e-40
+    tol = tol + HB * (np.abs(ref) + tol)
+    off = np.abs(f64(got) - ref)
+    assert (off <= tol).all(), f"{what}: {int((off > tol).sum())} off, worst {np.max(off / tol):.3g} of the bound"
+
+
+def check(B, H, T, d, dv, ld, s_qk=1.0, s_do=1.0):
+    g = torch.Generator("cuda").manual_seed(B * H + T)
+    q, k = ((s_qk * rand(g, B, T, H, d)).bfloat16().transpose(1, 2) for _ in range(2))
+    v = rand(g, B, T, H, dv).bfloat16().transpose(1, 2)
+    do = (s_do * rand(g, B, T, H, dv)).bfloat16().transpose(1, 2)
+    s0, dsT = s_qk * rand(g, B, H, d, dv), s_qk * s_do * rand(g, B, H, d, dv)
+    decay = torch.tensor([ld[h % len(ld)] for h in range(H)], device="cuda")
+    c = T + d + dv + 32 + 2.0 ** 9
+    o, _ = fwpkm.linear_attention(q, k, v, decay, 0.5, s0=s0)
+    grads = fwpkm.linear_attention_backward(q, k, v, decay, do, 0.5, s0=s0, d_sT=dsT)
+    fwpkm.linear_attention_sync()
+    x = [f64(t) for t in (q, k, v)]
+    a = [np.abs(t) for t in x]
+    dn, S, dS, D = f64(decay), f64(s0), f64(dsT), f64(do)
+    close(o, op.linear_attention(*x, dn, 0.5, S)[0], op.linear_attention(*a, dn, 0.5, np.abs(S))[0], c, "o")
+    ref = op.linear_attention_backward(*x, dn, D, 0.5, S, dS)
+    size = op.linear_attention_backward(*a, dn, np.abs(D), 0.5, np.abs(S), np.abs(dS))
+    for got, r, s, n in zip(grads[:3], ref, size, ("dq", "dk", "dv")):
+        close(got, r, s, c, n)
+
+
+@pytest.mark.parametrize("ld", [[-0.002, -0.1, -0.4, -3.0], [0.0, -0.01]])
+@pytest.mark.parametrize("B,H,T,d,dv", [(1, 4, 300, 128, 128), (1, 2, 1000, 128, 64), (20, 4, 150, 64, 128),
+                                        (2, 3, 257, 72, 104), (1, 1, 40, 64, 64)])
+def test_scores_and_states_keep_more_than_one_bf16_rounding(B, H, T, d, dv, ld):
+    check(B, H, T, d, dv, ld)
