@@ -30,7 +30,7 @@ struct ScanArgs {
   float* slots;
 };
 
-// a^e in fp32 from a log decay (e >= 0; a^0 = 1 for every a).
+// a^e in fp32 from a log decay (a^0 = 1 for every a).
 __device__ __forceinline__ float decay_pow(float log_decay, float e) { return e == 0.f ? 1.f : expf(log_decay * e); }
 
 // Length of sequence b.

@@ -9,9 +9,11 @@
 //   E' = a^m E + U
 // The descending pass is the same with the rows of the tile mirrored: its tiles end at the
 // chunk's first token, so every formula takes u = 127 - row.
-// a^(t-s) = R_t B_s with B_s = a^(127-s), R_t = a^(t-127), so P is weighted by column, E enters
-// as a^128 E, and R_t multiplies the finished row of O.  A head whose a^128 is out of range
-// (|log a^128| > LA_RANGE) takes the weights element by element and scales Q E in place.
+// a^(t-s) = R_t B_s with B_s = a^(63-s), R_t = a^(t-63), so P is weighted by column, E enters
+// as a^64 E, and R_t multiplies the finished row of O.  (About the middle of the chunk the weights
+// reach e^30 either way at most; about its end they reached e^-60, where scores of 1e-12 left
+// fp32's range.)  A head whose a^128 is out of range (|log a^128| > LA_RANGE) takes the weights
+// element by element and scales Q E in place.
 //
 // Precision: the inputs are bf16, exact operands.  P (weighted) and E enter their products as two
 // bf16 pieces, the upper half of the float and what that leaves (2^-16 left out at most), so O is off by
@@ -62,6 +64,7 @@ constexpr int LA_ROLE_REGS = 56, LA_KEY_REGS = 64, LA_SCORE_REGS = 64, LA_STATE_
 static_assert(LA_ROLE_WARPS * 32 * LA_ROLE_REGS + LA_GROUP * (LA_KEY_REGS + LA_SCORE_REGS + LA_STATE_REGS) <=
                   LA_THREADS * 72, "registers");
 constexpr uint64_t LA_TIMEOUT_NS = 200ull * 1000 * 1000;  // any single wait
+constexpr int LA_MID = LC / 2 - 1;       // the position that column weights count from
 constexpr float LA_RANGE = 60.f;         // largest |log a^128| taken through column weights
 constexpr int LA_BLOCK = LC * 128;       // bytes of a 64-column block of 128 rows
 
@@ -514,7 +517,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const int mt = threadIdx.x - LA_ROLE_WARPS * 32 - LA_GROUP;
     for (int j = mt; j <= LC; j += LA_GROUP) {
       pw[j] = decay_pow(ld, (float)j);
-      if (j < LC) bw[j] = fast ? decay_pow(ld, (float)(a.reverse ? j : LC - 1 - j)) : 1.f;
+      if (j < LC) bw[j] = fast ? decay_pow(ld, (float)(LA_MID - (a.reverse ? LC - 1 - j : j))) : 1.f;
     }
     asm volatile("bar.sync 1, %0;" ::"n"(LA_GROUP) : "memory");
     for (int c = 0; c < chunks && !local; ++c) {
@@ -663,12 +666,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const bool ready0 = g == 0 && a.in_ready;       // the first chunk's E is decayed already
     // (without a chunk nothing reads E, whose room the last state passes through)
     if (!local && chunks > 0) {
-      if (init) put_state(fast ? decay_pow(ld, (float)(LC - (ready0 ? 1 : 0))) : 1.f);
+      if (init) put_state(fast ? decay_pow(ld, (float)(LA_MID + 1 - (ready0 ? 1 : 0))) : 1.f);
       else if (lane == 0) mbar_arrive(&bar->est);
     }
+    const float a_mid = decay_pow(ld, (float)(LA_MID + 1));
     const float a_full = decay_pow(ld, (float)LC);
     // what multiplies a finished row of O
-    const float r_out = fast ? a.out_scale * expf(ld * (float)(a.reverse ? -row : row - (LC - 1))) : a.out_scale;
+    const float r_out = fast ? a.out_scale * expf(ld * (float)((a.reverse ? LC - 1 - row : row) - LA_MID)) : a.out_scale;
 
     for (int c = 0; c < chunks; ++c) {
       const uint32_t ph = c & 1;
@@ -695,7 +699,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       if (local) continue;
       if (c + 1 < chunks) {  // E in bf16, once Q E has read the one before
         if (!la_wait_warp(&bar->o1, ph, abort)) break;
-        put_state(fast ? a_full : 1.f);
+        put_state(fast ? a_mid : 1.f);
       }
       // O leaves: through the room of the chunk's V, which P V was the last to read, and TMA, or
       // (partial chunk) straight to its rows

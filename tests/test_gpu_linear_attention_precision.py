@@ -60,3 +60,10 @@ def check(B, H, T, d, dv, ld, s_qk=1.0, s_do=1.0):
                                         (2, 3, 257, 72, 104), (1, 1, 40, 64, 64)])
 def test_scores_and_states_keep_more_than_one_bf16_rounding(B, H, T, d, dv, ld):
     check(B, H, T, d, dv, ld)
+
+
+@pytest.mark.parametrize("s_qk,s_do", [(1e-8, 1.0), (1e-5, 1e-10), (1e6, 1e8)])
+@pytest.mark.parametrize("B,H,T,d,dv", [(1, 2, 300, 128, 128), (20, 4, 150, 64, 64), (1, 1, 600, 64, 128)])
+def test_inputs_of_any_size_on_heads_that_decay_quickly(B, H, T, d, dv, s_qk, s_do):
+    """Weights of up to |log a| 127 on one side of a chunk must not take small scores out of range."""
+    check(B, H, T, d, dv, [-0.46, -0.3], s_qk, s_do)
