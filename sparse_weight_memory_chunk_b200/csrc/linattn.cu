@@ -214,13 +214,7 @@ scan_kernel(ScanArgs a, int lj, int unit, int local) {
 
   T* op = (T*)a.o.p + (long long)b * a.o.sb + (long long)h * a.o.sh + c0;
   const float a1 = decay_pow(ld, 1.f);
-  // a^tb in two parts
-  float whole, rest;
-  {
-    const double w = exp((double)ld * tb);
-    whole = (float)w;
-    rest = (float)(w - (double)whole);
-  }
+  const float2 whole = decay_parts(ld, tb);
   int buf = 0;
   for (int tb0 = t0; tb0 < t1; tb0 += tb, buf ^= 1) {
     const int m = min(tb, t1 - tb0);
@@ -258,16 +252,11 @@ scan_kernel(ScanArgs a, int lj, int unit, int local) {
       }
     }
     // back to absolute: a^tb for the next batch's first token, a^(m-1) after the last token
-    float hi = whole, lo = rest;
-    if (last) {
-      const double w = m == 1 ? 1.0 : exp((double)ld * (m - 1));
-      hi = (float)w;
-      lo = (float)(w - (double)hi);
-    }
+    const float2 f = last ? decay_parts(ld, m - 1) : whole;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) S[i][x] = fmaf(S[i][x], hi, S[i][x] * lo);
+      for (int x = 0; x < 4; ++x) S[i][x] = fmaf(S[i][x], f.x, S[i][x] * f.y);
     if (!local) {
       __syncthreads();
       // warp u writes token u
@@ -335,9 +324,9 @@ step_kernel(ScanArgs a, int lj) {
     S[i] = i0 + i < a.d && j0 < a.dv ? *reinterpret_cast<const float4*>(src + (size_t)i * a.dv)
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
   if (tid == 0) {
-    const double w = exp((double)a.log_decay[h]);
-    sa[0] = (float)w;
-    sa[1] = (float)(w - (double)sa[0]);
+    const float2 w = decay_parts(a.log_decay[h], 1);
+    sa[0] = w.x;
+    sa[1] = w.y;
   }
   __syncthreads();
   const float hi = sa[0], lo = sa[1];
@@ -403,10 +392,7 @@ scan_combine_kernel(ScanArgs a) {
   const float ld = a.log_decay[h];
   for (int g = threadIdx.x; g < a.nseg - 1; g += 256) {
     const int len = max(0, min(n - g * a.seg_len, a.seg_len));
-    const int e = len - (g == 0 && a.in_ready && len > 0 ? 1 : 0);
-    const double w = e == 0 ? 1.0 : exp((double)ld * e);
-    decay[g].x = (float)w;
-    decay[g].y = (float)(w - (double)decay[g].x);
+    decay[g] = decay_parts(ld, len - (g == 0 && a.in_ready && len > 0 ? 1 : 0));
   }
   __syncthreads();
   if (x >= cells) return;

@@ -32,6 +32,13 @@ struct ScanArgs {
 
 // a^e in fp32 from a log decay (a^0 = 1 for every a).
 __device__ __forceinline__ float decay_pow(float log_decay, float e) { return e == 0.f ? 1.f : expf(log_decay * e); }
+// a^e in two fp32 parts, whose sum is exact to 2^-48: for a state that is multiplied by it again and again,
+// so that the rounding of one part does not compound.
+__device__ __forceinline__ float2 decay_parts(float log_decay, int e) {
+  const double w = e == 0 ? 1.0 : exp((double)log_decay * e);
+  const float hi = (float)w;
+  return make_float2(hi, (float)(w - (double)hi));
+}
 
 // Length of sequence b.
 __device__ __forceinline__ int scan_len(const ScanArgs& a, int b) {

@@ -21,7 +21,8 @@
 // chunk 0.5 us shorter).  The weighted keys of U are hi + mid + lo where the state is handed on in fp32 (exact to fp32),
 // else two pieces.  U adds the small pieces first, so few of the accumulator's roundings (which
 // truncate) are at full size: the state is 9e-8 off against 6e-7 the other way round.  E is
-// kept in fp32 registers and U is a fresh accumulator per chunk, so the tensor cores' running
+// kept in fp32 registers, a chunk's decay a number whose rounding is carried into the next chunk's (the same number
+// every time was off by up to 2^-25 a chunk, always the same way), and U is a fresh accumulator per chunk, so the tensor cores' running
 // sums span one chunk only.
 //
 // CTA = one head (and segment): warp 0 issues TMA loads and stores (K, V two stages, Q one, the
@@ -41,7 +42,7 @@
 // d = d_v = 128.)  A pass that only forms segment states has TMEM to spare and keeps two sets of
 // key pieces, so that weighting a chunk's keys overlaps the products of the one before.
 // Bound: for d = d_v = 128 a chunk is 128 KB, 3.0 us of an SM's share of the copy bandwidth; 148
-// heads of 8192 tokens take 4.7 us a chunk (64% of it), 5.0 with the final state: what is left is
+// heads of 8192 tokens take 4.8 us a chunk (62% of it), 5.2 with the final state: what is left is
 // the chain state -> E pieces -> Q E -> next state, and keys -> U -> next keys.
 #include <cstdio>
 
@@ -669,8 +670,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       if (init) put_state(fast ? decay_pow(ld, (float)(LA_MID + 1 - (ready0 ? 1 : 0))) : 1.f);
       else if (lane == 0) mbar_arrive(&bar->est);
     }
+    // a^128 is rounded for each chunk to where the chunks' product is nearest: what a rounding leaves is
+    // carried into the next one, so that it does not compound
+    const float2 a_full = decay_parts(ld, LC);
+    float left = 0.f;
     const float a_mid = decay_pow(ld, (float)(LA_MID + 1));
-    const float a_full = decay_pow(ld, (float)LC);
     // what multiplies a finished row of O
     const float r_out = fast ? a.out_scale * expf(ld * (float)((a.reverse ? LC - 1 - row : row) - LA_MID)) : a.out_scale;
 
@@ -682,7 +686,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       tc_fence_after();
       {
         const int len = m - (c == 0 && ready0 ? 1 : 0);
-        const float f = len == LC ? a_full : decay_pow(ld, (float)len);
+        float f;
+        if (len == LC) {
+          const float x = a_full.y + left;
+          f = a_full.x + x;
+          left = (a_full.x - f) + x;
+        } else {
+          f = decay_pow(ld, (float)len);
+        }
 #pragma unroll
         for (int q = 0; q < EC; q += 16) {
           uint32_t v[16];

@@ -67,3 +67,23 @@ def test_scores_and_states_keep_more_than_one_bf16_rounding(B, H, T, d, dv, ld):
 def test_inputs_of_any_size_on_heads_that_decay_quickly(B, H, T, d, dv, s_qk, s_do):
     """Weights of up to |log a| 127 on one side of a chunk must not take small scores out of range."""
     check(B, H, T, d, dv, [-0.46, -0.3], s_qk, s_do)
+
+
+@pytest.mark.parametrize("B,H,T", [(25, 3, 16384), (1, 8, 16384)])
+def test_a_state_decays_over_many_chunks(B, H, T):
+    """Keys in the first chunk only, so that the state after T tokens is a^(T - 128) times that after
+    128.  Each chunk rounds every element once, by at most u of it and in either direction: over the
+    4096 elements of a head the mean of T / 128 roundings has a standard deviation of at most
+    u / sqrt(3) sqrt(T / 128 / 4096) = 0.1 u; the bound is 2 u.  (a^128 as one fp32 number is off by
+    up to u / 2 in the same direction every time: 64 u here.)"""
+    g = torch.Generator("cuda").manual_seed(T)
+    k = torch.zeros(B, T, H, 64, device="cuda", dtype=torch.bfloat16)
+    k[:, :128] = rand(g, B, 128, H, 64).bfloat16()
+    k, v = k.transpose(1, 2), rand(g, B, T, H, 64).bfloat16().transpose(1, 2)
+    ld = -torch.exp(torch.linspace(-11.0, -7.0, H, device="cuda"))
+    first = fwpkm.linear_attention(*(x[:, :, :128] for x in (k, k, v)), ld, final_state=True)[1]
+    got = f64(fwpkm.linear_attention(k, k, v, ld, final_state=True)[1])
+    fwpkm.linear_attention_sync()
+    want = f64(first) * np.exp(f64(ld) * (T - 128))[None, :, None, None]
+    bias = ((got - want) * want).sum((2, 3)) / (want * want).sum((2, 3))
+    assert (np.abs(bias) <= 2 * U).all(), f"worst {np.abs(bias).max() / U:.3g} u"
