@@ -96,11 +96,12 @@ __device__ __forceinline__ float team_reduce(float x, float* red) {
   return x;
 }
 
-// v -> exp(v - max) over the team; returns 1 / their sum, 0 (v = 0) for a row without a finite
-// logit.  The maximum passes NaN by, but the sum keeps it.  exp is 2^(v log2 e - max log2 e),
-// one FMA and the hardware's 2^x (2^-22 relative; the FMA's rounding is that of v - max, and
-// that of max log2 e is common to the row): with expf, 32 values a lane, the instructions and
-// not the loads bounded both directions.
+// v -> exp(v - max) over the team; returns 1 / their sum, 0 (v = 0) for a row of -inf.  The maximum
+// passes NaN by, but the sum keeps it.  exp is 2^((v - max) log2 e) by the hardware's 2^x (2^-22
+// relative): with expf, 32 values a lane, the instructions and not the loads bounded both
+// directions.  The difference comes first, so that the row's largest term is 1 whatever its logits:
+// max log2 e rounded by itself is off by more than 2^x can hold from 4e9 on, and overflows for a row
+// filled with the type's lowest value.
 template <int NV, int L>
 __device__ __forceinline__ float team_exp(float (&v)[NV], float* red) {
   constexpr float LOG2E = 1.4426950408889634f;
@@ -108,12 +109,11 @@ __device__ __forceinline__ float team_exp(float (&v)[NV], float* red) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
   m = team_reduce<L, true>(m, red);
-  const bool none = m == -INFINITY;
-  const float shift = none ? 0.f : -m * LOG2E;
+  const float top = m == -INFINITY ? 0.f : m;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"(fmaf(v[i], LOG2E, shift)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((v[i] - top) * LOG2E));
     s += v[i];
   }
   s = team_reduce<L, false>(s, red);
