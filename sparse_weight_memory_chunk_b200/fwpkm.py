@@ -363,6 +363,15 @@ def _bytes(fn, where, *args):
     return out.value
 
 
+def _row_stride(t, axis, what):
+    """Elements between the rows of t along `axis`, rows being its last axis."""
+    width, ld = t.shape[-1], t.stride(axis)
+    if t.shape[axis] <= 1:
+        return max(ld, width)  # (of a single row any stride will do)
+    _need(ld >= width, f"{what}: the rows must not share memory (expand, unfold)")
+    return ld
+
+
 def _lookup_config(table, idx, w, scale):
     import torch
     _need(table.dim() == 2 and (table.stride(1) == 1 or table.shape[1] <= 1),
@@ -377,7 +386,7 @@ def _lookup_config(table, idx, w, scale):
         R, lead = idx.shape[-1], idx.shape[:-1]
         _side(w, table, torch.float32, idx.shape, "w")
     n = idx.numel() // R if R else 0
-    return LookupConfig(rows, max(table.stride(0), width), width, width, R, _dtype(table, "table"),
+    return LookupConfig(rows, _row_stride(table, 0, "table"), width, width, R, _dtype(table, "table"),
                         I64 if i64 else I32, scale), lead + (width,), n
 
 
@@ -414,9 +423,9 @@ def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumula
     if d_table is None:
         d_table = _empty(stream, table.shape, grad_dtype or table.dtype, table)
     _need(d_table.shape == table.shape and d_table.device == table.device
-          and (d_table.stride(1) == 1 or table.shape[1] <= 1)
-          and (table.shape[0] <= 1 or d_table.stride(0) >= table.shape[1]),
-          "d_table must have the table's shape and device, its rows contiguous and apart")
+          and (d_table.stride(1) == 1 or table.shape[1] <= 1),
+          "d_table must have the table's shape and device, its rows contiguous")
+    grad_ld = _row_stride(d_table, 0, "d_table")
     _need(grad_dtype is None or d_table.dtype == grad_dtype, "d_table is not of grad_dtype")
     if w is None or not need_dw:
         _need(dw is None, "dw needs w and need_dw")
@@ -429,7 +438,7 @@ def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumula
                             _bytes(L.fwpkm_lookup_backward_workspace_size, "lookup_backward", c, n), table,
                             stream, "lookup_backward")
     _call(table, stream, "lookup_backward", L.fwpkm_lookup_backward, c, table.data_ptr(), idx.data_ptr(),
-          None if w is None else w.data_ptr(), p_out, n, d_table.data_ptr(), max(d_table.stride(0), table.shape[1]),
+          None if w is None else w.data_ptr(), p_out, n, d_table.data_ptr(), grad_ld,
           _dtype(d_table, "d_table"), int(accumulate), None if dw is None else dw.data_ptr(), pw, nw)
     return d_table, dw
 
@@ -455,7 +464,7 @@ def _balance_config(x, idx, mask, kind, coef):
     if mask is not None:
         _need(mask.dtype in (torch.bool, torch.uint8), "mask must be bool or uint8")
         _side(mask, x, mask.dtype, (G, T), "mask")
-    return BalanceConfig(T, max(x.stride(1), E), x.stride(0) if G > 1 else 0, G, E, k, _dtype(x, "x"),
+    return BalanceConfig(T, _row_stride(x, 1, "x"), x.stride(0) if G > 1 else 0, G, E, k, _dtype(x, "x"),
                          BALANCE_KIND[kind], coef)
 
 
