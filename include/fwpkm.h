@@ -418,7 +418,8 @@ typedef struct {
   float scale;
 } fwpkm_lookup_config;
 
-/* out [n][width] of n tokens.  w is fp32 or NULL.  n = 0 is a no-op. */
+/* out [n][width] of n tokens.  w is fp32 or NULL.  n = 0 is a no-op.  out must not be the memory of
+ * the table or of w. */
 fwpkm_status fwpkm_lookup(const fwpkm_lookup_config* cfg, const void* table, const void* idx, const float* w,
                           long long n, void* out, void* stream);
 
@@ -431,7 +432,9 @@ fwpkm_status fwpkm_lookup_backward_workspace_size(const fwpkm_lookup_config* cfg
  *            formed (then the workspace may be NULL).  accumulate = 0: every row is written
  *            (zero where nothing was read; also for n = 0); else the gradient is added to
  *            the rows that were read and the others are left as they were.
- *   dw       fp32 [n][R] or NULL; needs the table.
+ *   dw       fp32 [n][R] or NULL; needs the table.  It is written before d_table's sums read w:
+ *            beside a d_table it must share no memory with w.  Neither dw nor d_table may be the
+ *            memory of d_out, nor dw that of the table, nor d_table that of w.
  *   table    read for dw only (else may be NULL); d_table may be the table itself (accumulate
  *            with a negative scale: a step of gradient descent), dw is formed before.
  * The pairs are sorted by row, so each row's terms are summed in a fixed order.  The

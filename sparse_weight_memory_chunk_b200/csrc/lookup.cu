@@ -1056,7 +1056,7 @@ fwpkm_status fwpkm_lookup(const fwpkm_lookup_config* cfg, const void* table, con
   if (n == 0) return FWPKM_OK;
   const size_t es = dsize(cfg->dtype);
   if (!table || !idx || !out || !ptr_al(table, es) || !ptr_al(out, es) || (w && !ptr_al(w, 4)) ||
-      !ptr_al(idx, cfg->idx_dtype == FWPKM_I64 ? 8 : 4))
+      !ptr_al(idx, cfg->idx_dtype == FWPKM_I64 ? 8 : 4) || out == table || out == w)
     return FWPKM_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   cudaGetLastError();
@@ -1098,6 +1098,11 @@ fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* t
       if (!workspace || !ptr_al(workspace, 256)) return FWPKM_ERR_INVALID_ARG;
       if (ws_bytes < back_carve(*cfg, n * cfg->R, nullptr, nullptr)) return FWPKM_ERR_WORKSPACE;
     }
+    // outputs in the memory of what is still to be read (the table is not, once dw is formed)
+    const uintptr_t w0 = (uintptr_t)w, dw0 = (uintptr_t)dw, bytes = 4 * (uintptr_t)(n * cfg->R);
+    if (d_table && (d_table == d_out || d_table == w || (w && dw && dw0 < w0 + bytes && w0 < dw0 + bytes)))
+      return FWPKM_ERR_INVALID_ARG;
+    if (dw && (dw == d_out || dw == table)) return FWPKM_ERR_INVALID_ARG;
   }
   if (n == 0 && (!d_table || accumulate)) return FWPKM_OK;
   cudaStream_t s = (cudaStream_t)stream;
