@@ -530,6 +530,10 @@ fwpkm_status fwpkm_balance_loss_backward(const fwpkm_balance_config* cfg, const 
   const size_t es = bal_es(cfg->dtype);
   if (!x || !slope || !dx || !bal_al(x, es) || !bal_al(dx, es) || !bal_al(slope, 4) || (d_loss && !bal_al(d_loss, 4)))
     return FWPKM_ERR_INVALID_ARG;
+  // (in place a row is read and written by the same threads, but only where dx's rows are x's)
+  if (dx == x && ((cfg->ld != cfg->experts && cfg->tokens > 1) ||
+                  (cfg->group_stride != cfg->tokens * cfg->experts && cfg->groups > 1)))
+    return FWPKM_ERR_INVALID_ARG;
   cudaGetLastError();
   PdlScope pdl(true);
   BalRun r = {};
