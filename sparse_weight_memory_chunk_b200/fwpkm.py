@@ -332,14 +332,15 @@ def _side(t, like, dtype, shape, what):
     return t.data_ptr()
 
 
-def _empty(stream, shape, dtype, like):
+def _empty(stream, shape, dtype, like, zero=False):
     """A new tensor on `like`'s device.  With a stream given it comes from that stream's memory:
     the current one's may still be in use, or be handed out again, while the call runs there."""
     import torch
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return make(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return make(shape, dtype=dtype, device=like.device)
 
 
 def _scratch(workspace, nbytes, like, stream, what):
@@ -530,9 +531,10 @@ def _linattn_args(q, k, v, log_decay, scale, lens):
     return ctypes.byref(LinattnConfig(B, H, d, dv, _dtype(q, "q"), scale)), hq, hk, hv, ld, ln, B, H, T, d, dv, like
 
 
-def _rows_like(t, B, H, T, w, stream):
-    """A new [B][H][T][w] tensor in the memory order [B][T][H][w] of a projection's output."""
-    return _empty(stream, (B, T, H, w), t.dtype, t).transpose(1, 2)
+def _rows_like(t, B, H, T, w, stream, lens):
+    """A new [B][H][T][w] tensor in the memory order [B][T][H][w] of a projection's output; with
+    lengths it holds zeros, which stay behind a sequence's end."""
+    return _empty(stream, (B, T, H, w), t.dtype, t, lens is not None).transpose(1, 2)
 
 
 def linear_attention_workspace_size(q, v, backward=False) -> int:
@@ -546,11 +548,11 @@ def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, 
     """fwpkm_linear_attention: (o, sT) of q, k [B][H][T][d], v [B][H][T][d_v] (any strides with
     contiguous rows), log_decay [H] fp32, start states s0 [B][H][d][d_v] fp32 and lengths lens
     [B] int32.  sT is None unless given or asked for with final_state.  Rows of o behind a
-    sequence's end are left as they were (a new o holds anything there)."""
+    sequence's end are left as they were (zeros in a new o)."""
     import torch
     c, hq, hk, hv, ld, ln, B, H, T, d, dv, like = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
-        o = _rows_like(v, B, H, T, dv, stream)
+        o = _rows_like(v, B, H, T, dv, stream, lens)
     ho = _heads(o, *like, (B, H, T, dv), "o")
     if sT is None and final_state:
         sT = _empty(stream, (B, H, d, dv), torch.float32, q)
@@ -568,12 +570,12 @@ def linear_attention_backward(q, k, v, log_decay, d_o, scale=1.0, s0=None, d_sT=
                               state_grad=True, workspace=None, stream=None):
     """fwpkm_linear_attention_backward: (dq, dk, dv, ds0) of linear_attention from d_o and the
     final state's gradient d_sT (None: zero).  `grads`: (dq, dk, dv) to fill; ds0 is None with
-    state_grad=False.  Rows behind a sequence's end are left as they were."""
+    state_grad=False.  Rows behind a sequence's end are left as they were (zeros in new gradients)."""
     import torch
     c, hq, hk, hv, ld, ln, B, H, T, d, dv, like = _linattn_args(q, k, v, log_decay, scale, lens)
     ho = _heads(d_o, *like, (B, H, T, dv), "d_o")
     if grads is None:
-        grads = tuple(_rows_like(q, B, H, T, w, stream) for w in (d, d, dv))
+        grads = tuple(_rows_like(q, B, H, T, w, stream, lens) for w in (d, d, dv))
     hg = [_heads(t, *like, (B, H, T, w), n) for t, w, n in zip(grads, (d, d, dv), ("dq", "dk", "dv"))]
     if ds0 is None and state_grad:
         ds0 = _empty(stream, (B, H, d, dv), torch.float32, q)
@@ -593,11 +595,12 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
                           stream=None):
     """fwpkm_linear_attention_step: (o, new state) of a few new tokens [B][H][n][..] from the
     states [B][H][d][d_v], which are updated in place unless state_out is given or
-    in_place=False (then a new tensor is)."""
+    in_place=False (then a new tensor is).  Rows of o behind a sequence's end are left as they
+    were (zeros in a new o)."""
     import torch
     c, hq, hk, hv, ld, ln, B, H, T, d, dv, like = _linattn_args(q, k, v, log_decay, scale, lens)
     if o is None:
-        o = _rows_like(v, B, H, T, dv, stream)
+        o = _rows_like(v, B, H, T, dv, stream, lens)
     ho = _heads(o, *like, (B, H, T, dv), "o")
     _need(state is not None, "state is needed")
     ps = _side(state, q, torch.float32, (B, H, d, dv), "state")
