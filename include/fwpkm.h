@@ -560,8 +560,8 @@ fwpkm_status fwpkm_linear_attention_step(const fwpkm_linattn_config* cfg, const 
                                          float* state_out, void* stream);
 
 /* Wait for `stream` and return the device status that linear-attention kernels on the current
- * device have latched since the last call (FWPKM_ERR_TIMEOUT: a bounded wait ran out and that
- * call's results are not valid), clearing it. */
+ * device have latched since the last call (FWPKM_ERR_TIMEOUT: a bounded wait ran out; the rows,
+ * gradients and states of the heads it ran out for are NaN), clearing it. */
 fwpkm_status fwpkm_linear_attention_sync(void* stream);
 
 /* Wait for `stream` and return the latched device status (FWPKM_OK,

@@ -789,6 +789,24 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     tc_fence_after();
     tmem_dealloc(tmem, TM_COLS);
   }
+  if (*abort) {
+    // what this CTA owes is NaN, so that nothing passes for a result before the status is read (the
+    // rows' stores have been waited for by the warp that issued them).  Where it is, is found anew:
+    // kept in registers until here, it would cost the passes 1%
+    int bh, g;
+    asm volatile("mov.u32 %0, %%ctaid.x;\n mov.u32 %1, %%ctaid.y;" : "=r"(bh), "=r"(g));
+    const int b = bh / a.H, h = bh - b * a.H, n = scan_len(a, b);
+    const int t0 = min(n, g * a.seg_len), t1 = min(n, t0 + a.seg_len), first = a.reverse ? n - t1 : t0;
+    const size_t cells = (size_t)a.d * a.dv;
+    for (long long x = threadIdx.x; !local && x < (long long)(t1 - t0) * a.dv; x += LA_THREADS) {
+      const long long t = first + x / a.dv;
+      const int j = (int)(x % a.dv);
+      ((unsigned short*)a.o.p)[(long long)b * a.o.sb + (long long)h * a.o.sh + t * a.o.st + j] = 0x7fff;
+    }
+    float* dst = local ? a.slots + ((size_t)bh * a.nseg + g) * cells
+                       : (a.s_out && g == a.nseg - 1 ? a.s_out + (size_t)bh * cells : nullptr);
+    for (size_t x = threadIdx.x; dst && x < cells; x += LA_THREADS) dst[x] = __int_as_float(0x7fffffff);
+  }
   if (threadIdx.x == 0 && *abort) raise_status(&g_la_status, nullptr, DEV_TIMEOUT);
 }
 

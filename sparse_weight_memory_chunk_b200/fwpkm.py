@@ -613,7 +613,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
 
 def linear_attention_sync(device=None, stream=None):
     """fwpkm_linear_attention_sync: wait for the stream and raise what linear-attention kernels
-    on the device have latched (a wait that timed out)."""
+    on the device have latched (a wait that timed out: what its heads should have given is NaN)."""
     import torch
     with torch.cuda.device(device if stream is None else stream.device):
         handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
