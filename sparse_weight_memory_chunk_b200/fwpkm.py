@@ -343,6 +343,15 @@ def _empty(stream, shape, dtype, like, zero=False):
         return make(shape, dtype=dtype, device=like.device)
 
 
+def _zero(stream, *tensors):
+    """The outputs of sums without a term (a table without rows, a bag without entries)."""
+    import torch
+    for t in tensors:
+        _need(t.is_cuda, "the tensors must be on a CUDA device")
+        with torch.cuda.stream(stream):
+            t.zero_()
+
+
 def _scratch(workspace, nbytes, like, stream, what):
     """(tensor, pointer, bytes) of a workspace: the caller's, or a new one of nbytes."""
     if workspace is None:
@@ -367,10 +376,11 @@ def _bytes(fn, where, *args):
 def _row_stride(t, axis, what):
     """Elements between the rows of t along `axis`, rows being its last axis."""
     width, ld = t.shape[-1], t.stride(axis)
-    if t.shape[axis] <= 1:
-        return max(ld, width)  # (of a single row any stride will do)
-    _need(ld >= width, f"{what}: the rows must not share memory (expand, unfold)")
-    return ld
+    if ld >= width:
+        return ld
+    if t.shape[axis] > 1:
+        raise ValueError(f"{what}: the rows must not share memory (expand, unfold)")
+    return width  # (of a single row any stride will do)
 
 
 def _lookup_config(table, idx, w, scale):
@@ -386,7 +396,7 @@ def _lookup_config(table, idx, w, scale):
         _need(idx.dim() >= 1, "with w the last axis of idx is the bag")
         R, lead = idx.shape[-1], idx.shape[:-1]
         _side(w, table, torch.float32, idx.shape, "w")
-    n = idx.numel() // R if R else 0
+    n = idx.numel() // R if R and rows else None  # (None: no sum has a term)
     return LookupConfig(rows, _row_stride(table, 0, "table"), width, width, R, _dtype(table, "table"),
                         I64 if i64 else I32, scale), lead + (width,), n
 
@@ -394,12 +404,16 @@ def _lookup_config(table, idx, w, scale):
 def lookup(table, idx, w=None, scale=1.0, out=None, stream=None):
     """fwpkm_lookup: scale * table[idx], shape idx.shape + [width]; with weights w (fp32, the
     shape of idx) the last axis of idx is summed: scale * sum_r w[.., r] table[idx[.., r]].
-    Indices outside the table read zeros."""
+    Indices outside the table read zeros, and so do all in a table without rows and bags without
+    entries."""
     cfg, shape, n = _lookup_config(table, idx, w, scale)
     if out is None:
         out = _empty(stream, shape, table.dtype, table)
     else:
         _side(out, table, table.dtype, shape, "out")
+    if n is None:
+        _zero(stream, out)
+        return out
     _call(table, stream, "lookup", lib().fwpkm_lookup, ctypes.byref(cfg), table.data_ptr(), idx.data_ptr(),
           None if w is None else w.data_ptr(), n, out.data_ptr())
     return out
@@ -407,6 +421,8 @@ def lookup(table, idx, w=None, scale=1.0, out=None, stream=None):
 
 def lookup_backward_workspace_size(table, idx, w=None) -> int:
     cfg, _, n = _lookup_config(table, idx, w, 1.0)
+    if n is None:
+        return 0
     return _bytes(lib().fwpkm_lookup_backward_workspace_size, "lookup_backward_workspace_size", ctypes.byref(cfg), n)
 
 
@@ -434,6 +450,9 @@ def lookup_backward(table, idx, d_out, w=None, scale=1.0, d_table=None, accumula
         dw = _empty(stream, idx.shape, torch.float32, table)
     else:
         _side(dw, table, torch.float32, idx.shape, "dw")
+    if n is None:
+        _zero(stream, *(t for t in (None if accumulate else d_table, dw) if t is not None))
+        return d_table, dw
     L, c = lib(), ctypes.byref(cfg)
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
                             _bytes(L.fwpkm_lookup_backward_workspace_size, "lookup_backward", c, n), table,
@@ -476,14 +495,16 @@ def balance_loss(x, idx=None, mask=None, kind="load", coef=1.0, workspace=None, 
     import torch
     cfg = _balance_config(x, idx, mask, kind, coef)
     G, E = cfg.groups, cfg.experts
-    L, c = lib(), ctypes.byref(cfg)
-    keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
-                            _bytes(L.fwpkm_balance_workspace_size, "balance_loss", c), x, stream, "balance_loss")
     r = BalanceLoss()
     r.kind, r.coef = kind, coef
     r.loss = _empty(stream, G, torch.float32, x)
     r.usage, r.slope = _empty(stream, (G, E), torch.float32, x), _empty(stream, (G, E), torch.float32, x)
     r.counts = None if idx is None else _empty(stream, (G, E), torch.int32, x)
+    if not G:
+        return r
+    L, c = lib(), ctypes.byref(cfg)
+    keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
+                            _bytes(L.fwpkm_balance_workspace_size, "balance_loss", c), x, stream, "balance_loss")
     _call(x, stream, "balance_loss", L.fwpkm_balance_loss, c, x.data_ptr(), None if idx is None else idx.data_ptr(),
           None if mask is None else mask.data_ptr(), pw, nw, r.loss.data_ptr(),
           None if idx is None else r.counts.data_ptr(), r.usage.data_ptr(), r.slope.data_ptr())
@@ -502,6 +523,8 @@ def balance_loss_backward(x, result: BalanceLoss, mask=None, d_loss=None, dx=Non
         dx = _empty(stream, (G, T, E), x.dtype, x)
     else:
         _side(dx, x, x.dtype, (G, T, E), "dx")
+    if not G:
+        return dx
     _call(x, stream, "balance_loss_backward", lib().fwpkm_balance_loss_backward, ctypes.byref(cfg), x.data_ptr(),
           None if mask is None else mask.data_ptr(), ps, pl, dx.data_ptr())
     return dx
@@ -539,6 +562,8 @@ def _rows_like(t, B, H, T, w, stream, lens):
 
 def linear_attention_workspace_size(q, v, backward=False) -> int:
     cfg = LinattnConfig(q.shape[0], q.shape[1], q.shape[3], v.shape[3], _dtype(q, "q"), 1.0)
+    if not cfg.B * cfg.H:
+        return 0
     return _bytes(lib().fwpkm_linear_attention_workspace_size, "linear_attention_workspace_size", ctypes.byref(cfg),
                   q.shape[2], int(backward))
 
@@ -558,6 +583,8 @@ def linear_attention(q, k, v, log_decay, scale=1.0, s0=None, lens=None, o=None, 
         sT = _empty(stream, (B, H, d, dv), torch.float32, q)
     p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
     pT = _side(sT, q, torch.float32, (B, H, d, dv), "sT")
+    if not B * H:
+        return o, sT
     L = lib()
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
                             _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention", c, T, 0), q, stream,
@@ -582,6 +609,8 @@ def linear_attention_backward(q, k, v, log_decay, d_o, scale=1.0, s0=None, d_sT=
     p0 = _side(s0, q, torch.float32, (B, H, d, dv), "s0")
     pT = _side(d_sT, q, torch.float32, (B, H, d, dv), "d_sT")
     pd = _side(ds0, q, torch.float32, (B, H, d, dv), "ds0")
+    if not B * H:
+        return (*grads, ds0)
     L = lib()
     keep, pw, nw = _scratch(workspace, 0 if workspace is not None else
                             _bytes(L.fwpkm_linear_attention_workspace_size, "linear_attention_backward", c, T, 1), q, stream,
@@ -607,6 +636,8 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, lens=None, o=Non
     if state_out is None:
         state_out = state if in_place else _empty(stream, state.shape, torch.float32, q)
     po = _side(state_out, q, torch.float32, (B, H, d, dv), "state_out")
+    if not B * H:
+        return o, state_out
     _call(q, stream, "linear_attention_step", lib().fwpkm_linear_attention_step, c, hq, hk, hv, T, ld, ln, ps, ho, po)
     return o, state_out
 
