@@ -1120,6 +1120,9 @@ fwpkm_status fwpkm_lookup_backward(const fwpkm_lookup_config* cfg, const void* t
     const BackWork* w = d_table ? &bw : nullptr;
     nl = bf ? go_pairs_t<__nv_bfloat16>(*cfg, idx, P, w, &at, g, s) : go_pairs_t<float>(*cfg, idx, P, w, &at, g, s);
     if (nl < 0) return FWPKM_ERR_CUDA;
+    // (the sums take rows to write from the sorted pairs: where a launch above was refused, those are
+    // whatever the workspace held)
+    if (cudaPeekAtLastError() != cudaSuccess) return done(0);
   }
   if (d_table) {
     SegArgs a = {};
