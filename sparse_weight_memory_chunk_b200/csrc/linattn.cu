@@ -21,7 +21,7 @@
 // multiplication per batch and its rounding does not compound over the tokens; a head whose
 // a^-SC_TB would leave fp32's range takes batches of one token.  Bound: instruction issue
 // (194 a warp and token at d = d_v = 128, of them 64 packed FMAs): 256 heads of 512 tokens in
-// 350 us, 49 TFLOP/s.  (With rows staged by plain loads between two barriers the loads'
+// 350 us, 24.5 TFLOP/s.  (With rows staged by plain loads between two barriers the loads'
 // latency bounded it: 128 such heads in 665 us, now 232.)
 #include <cmath>
 #include <cstdio>
@@ -308,7 +308,6 @@ step_kernel(ScanArgs a, int lj) {
   __shared__ float sa[2];
   pdl_wait();
   pdl_trigger();
-  const int rgn = SC_THREADS / lj;
   const int cols = 4 * lj, tiles = (a.dv + cols - 1) / cols;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int jl = tid & (lj - 1), i0 = (tid / lj) * NI;

@@ -75,7 +75,7 @@ def test_a_state_decays_over_many_chunks(B, H, T):
     128.  Each chunk rounds every element once, by at most u of it and in either direction: over the
     4096 elements of a head the mean of T / 128 roundings has a standard deviation of at most
     u / sqrt(3) sqrt(T / 128 / 4096) = 0.1 u; the bound is 2 u.  (a^128 as one fp32 number is off by
-    up to u / 2 in the same direction every time: 64 u here.)"""
+    its rounding and expf's in the same direction every time: up to 124 u here.)"""
     g = torch.Generator("cuda").manual_seed(T)
     k = torch.zeros(B, T, H, 64, device="cuda", dtype=torch.bfloat16)
     k[:, :128] = rand(g, B, 128, H, 64).bfloat16()
